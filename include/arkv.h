@@ -28,7 +28,8 @@
  *
  * Conventions.
  *   - Every pointer is a device pointer the caller owns and allocated, except
- *     where a comment says "host".  The library allocates nothing and keeps no
+ *     where a comment says "host"; it and the stream belong to the calling
+ *     thread's current device.  The library allocates nothing and keeps no
  *     global state; calls on different streams with different buffers are
  *     independent.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
@@ -64,6 +65,7 @@ typedef struct CUstream_st *arkv_stream_t;   /* same type as cudaStream_t */
 #define ARKV_STATUS_BF16_FULL  1   /* an append found the bf16 segment full; token dropped */
 #define ARKV_STATUS_FP8_FULL   2   /* a reassignment found the fp8 segment full; demotion became eviction */
 #define ARKV_STATUS_TIMEOUT    4   /* a kernel gave up waiting for its own bulk copy (a bug, never expected) */
+#define ARKV_STATUS_BAD_FORK   8   /* a sequence's source was out of range, or itself overwritten in place; left as it was */
 
 #define ARKV_TIER_ORIGINAL   0
 #define ARKV_TIER_QUANTIZED  1
@@ -258,6 +260,96 @@ int arkv_copy_async(void *dst, const void *src, size_t bytes, arkv_stream_t stre
 #define ARKV_NOALLOC_SCRATCH_BYTES (24u << 20)
 int arkv_reassign_noalloc(const arkv_cfg *cfg, int32_t step, float r, const int32_t *ctx_len,
                           arkv_layer_cache *cache, uint8_t *tier_dbg, arkv_stream_t stream);
+
+/* The queries, keys and values of `n_tok` tokens of every sequence from the rows of a
+ * fused projection: RMS norm of every query and key head (optional), rotation by
+ * position, and the layouts the other calls take, in one pass.
+ * For every token t and head x of D dimensions
+ *   y = x / sqrt(mean(x^2) + eps) * w          (w = q_weight or k_weight; y = x if null)
+ *   (y_a, y_b) -> (y_a cos f - y_b sin f, y_a sin f + y_b cos f),  f = position * freq[i]
+ * for the rot / 2 pairs (a, b) = (i, i + rot / 2), or (2i, 2i + 1) if interleaved; the
+ * dimensions from rot on are not rotated.  Values are copied.  float32 arithmetic, the
+ * angle reduced exactly (64-bit turns), one rounding to bf16.  The paper has no
+ * counterpart: this is the step before arkv_decode_attn and arkv_prefill_stats in a
+ * model whose attention rotates (and, Qwen3-like, normalises) its heads.
+ *   qkv      row (b n_tok + t) at qkv + row * qkv_stride (elements, a multiple of 8, at least
+ *            (hq + 2 hkv) D): hq query heads, hkv key heads, hkv value heads; bf16 bits
+ *   pos0     [batch] int32 (nullable: 0); token t of sequence b is at pos0[b] + step + t
+ *            (a decode step: n_tok = 1, pos0 = ctx_len)
+ *   length   [batch] int32 (nullable: n_tok): tokens t >= length[b] are padding, whose
+ *            rows are not read and whose outputs stay as they were
+ *   q_weight, k_weight  [D] bf16 bits, each nullable (no norm of those heads); eps >= 0
+ *   freq     [rot / 2] double, radians per position (nullable if rot = 0); rot even, 0..D
+ *   q [batch][hq][n_stride][D], k, v [batch][hkv][n_stride][D] bf16 bits, token t at
+ *            index t, n_stride >= n_tok; q nullable
+ *   q_obs    [batch][hq][n_obs][D] (nullable): the queries of the last min(n_obs, length)
+ *            tokens of each sequence, the last one at index n_obs - 1 (arkv_prefill_stats)
+ * qkv and the outputs 16-byte aligned; the outputs overlap neither qkv nor each other.
+ * Of cfg only batch, hq, hkv, head_dim and n_obs matter. */
+int arkv_qk_norm_rope(const arkv_cfg *cfg, int32_t n_tok, const uint16_t *qkv, int64_t qkv_stride,
+                      const int32_t *pos0, int32_t step, const int32_t *length,
+                      const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                      const double *freq, int32_t rot, int32_t interleaved, int32_t n_stride,
+                      uint16_t *q, uint16_t *k, uint16_t *v, uint16_t *q_obs, arkv_stream_t stream);
+
+/* Copies, forks and frees the sequences of a packed cache: sequence b of dst becomes a copy
+ * of sequence src_seq[b] of src -- every live slot in its place, with codes, scales,
+ * positions, score state and counts -- so that it can go on from there (parallel samples
+ * of one prompt, beams, a state kept before a speculative step).
+ *   src_seq [dst batch] int32 (device): a sequence of src, ARKV_SEQ_FREE (its counts become
+ *   0) or ARKV_SEQ_KEEP (it stays as it is).
+ * dst and src are two caches with disjoint buffers, or the same cache (the same buffers and
+ * configuration): then a sequence may only be copied if it keeps its own state in this call
+ * (src_seq[s] = s or ARKV_SEQ_KEEP).  A sequence with another src_seq, or whose source does
+ * not keep its state, stays as it was and ARKV_STATUS_BAD_FORK is set.
+ * Slots past a count stay as they were.  The two configurations agree in hkv, head_dim and
+ * quant_format; batch and capacities may differ: the slots past a smaller capacity are
+ * dropped and ARKV_STATUS_BF16_FULL or ARKV_STATUS_FP8_FULL is set.  The bits are set in
+ * *dst->status. */
+#define ARKV_SEQ_FREE  (-1)
+#define ARKV_SEQ_KEEP  (-2)
+int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_cfg *src_cfg,
+                    const arkv_layer_cache *src, const int32_t *src_seq, arkv_stream_t stream);
+
+/* Decode attention to prefixes that several sequences (branches) share, read once for all
+ * the branches of a prefix, and joined with each branch's attention to its own tokens.
+ * cfg describes the branches, prefix_cfg the prefixes: `prefix` is a packed cache (as
+ * arkv_quantize_pack leaves it) whose sequences are the prefixes; hq, hkv and head_dim
+ * agree.  Branches branch_start[p] .. branch_start[p + 1] - 1 share prefix p
+ * (branch_start [prefix batch + 1] int32, device, not decreasing, within 0..batch;
+ * nullable with one prefix: every branch); other branches have no prefix.
+ * For query head h of a branch, with k^, v^ the prefix's live tokens as arkv_decode_attn
+ * reads them and raw_k = q_h . k^_k,
+ *   M = max(M_own, max_k raw_k),  w = L_own exp((M_own - M) / sqrt(D)),
+ *   L = w + sum_k exp((raw_k - M) / sqrt(D)),
+ *   o = (w o_own + sum_k exp((raw_k - M) / sqrt(D)) v^_k) / L.
+ *   q      [batch][hq][D] bf16 bits
+ *   o_own  [batch][hq][D] float: the branch's own attention (arkv_decode_attn's o)
+ *   ml_own [batch * hkv][4][2] float: (M, L) of its heads, head j of group g of branch b at
+ *          [b hkv + g][j] (arkv_decode_ml); a head with L = 0 has no own tokens.  o_own and
+ *          ml_own are both given or both null (no own tokens)
+ *   o      [batch][hq][D] bf16 bits, as the output projection reads it
+ *   ml     [batch * hkv][4][2] float (nullable): the joined (M, L) of the hq / hkv heads of
+ *          each group.  ml may be ml_own: with the address of arkv_decode_ml for both,
+ *          the arkv_score_update that follows sees the whole softmax
+ * A head without any token gets o = 0 and (M, L) = (-inf, 0).  A probability enters the
+ * product with V rounded to bf16 (the rounding of o itself); sums are float32.
+ * The prefix is only read: its tokens are neither scored nor reassigned while it is
+ * shared.  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
+ * The workspace holds at least arkv_prefix_workspace_bytes() bytes and needs no
+ * preparation.  Launched as a programmatic dependent like arkv_decode_attn: with
+ * cfg->early_start = 1 it reads the prefix cache and branch_start before the previous
+ * kernel on the stream has finished. */
+size_t arkv_prefix_workspace_bytes(const arkv_cfg *cfg, const arkv_cfg *prefix_cfg);
+int arkv_prefix_attn(const arkv_cfg *cfg, const arkv_cfg *prefix_cfg, const uint16_t *q,
+                     const arkv_layer_cache *prefix, const int32_t *branch_start,
+                     const float *o_own, const float *ml_own, uint16_t *o, float *ml, void *ws,
+                     size_t ws_bytes, arkv_stream_t stream);
+
+/* The (M, L) of every head that arkv_decode_attn leaves in its workspace `ws` for
+ * arkv_score_update: *ml = [batch * hkv][4][2] float within ws (p = exp((raw - M) /
+ * sqrt(D)) / L).  Host only. */
+int arkv_decode_ml(const arkv_cfg *cfg, void *ws, size_t ws_bytes, float **ml);
 
 /* Message of the calling thread's last failure ("" if none). */
 const char *arkv_last_error_string(void);

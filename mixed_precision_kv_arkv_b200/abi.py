@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libarkv.so"
 
 ARKV_OK, ARKV_EINVAL, ARKV_ECAPACITY, ARKV_ECUDA = 0, -1, -2, -3
 ARKV_STATUS_BF16_FULL, ARKV_STATUS_FP8_FULL = 1, 2
+ARKV_STATUS_TIMEOUT, ARKV_STATUS_BAD_FORK = 4, 8
+ARKV_SEQ_FREE, ARKV_SEQ_KEEP = -1, -2
 ARKV_TIER_ORIGINAL, ARKV_TIER_QUANTIZED, ARKV_TIER_EVICTED = 0, 1, 2
 ARKV_WS_DECODE, ARKV_WS_REASSIGN, ARKV_WS_PREFILL = 0, 1, 2
 ARKV_FMT_E4M3, ARKV_FMT_E5M2 = 0, 1
@@ -59,6 +61,13 @@ _SIG = {
     "arkv_fp8_encode": (ctypes.c_int, [ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
     "arkv_copy_async": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "arkv_reassign_noalloc": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_float, _P, _P, _P, _P]),
+    "arkv_qk_norm_rope": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int32, _P,
+                                         _P, _P, ctypes.c_float, _P, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_int32, _P, _P, _P, _P, _P]),
+    "arkv_cache_fork": (ctypes.c_int, [_P, _P, _P, _P, _P, _P]),
+    "arkv_prefix_workspace_bytes": (ctypes.c_size_t, [_P, _P]),
+    "arkv_prefix_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "arkv_decode_ml": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "arkv_last_error_string": (ctypes.c_char_p, []),
 }
 
@@ -155,3 +164,33 @@ def arkv_copy_async(dst, src, nbytes, stream, check=True) -> int:
 def arkv_fp8_encode(fmt, x, out, n, stream, check=True) -> int:
     rc = lib().arkv_fp8_encode(fmt, x, out, n, stream)
     return _check("arkv_fp8_encode", rc) if check else rc
+
+
+def arkv_qk_norm_rope(cfg, n_tok, qkv, qkv_stride, pos0, step, length, q_weight, k_weight, eps, freq, rot,
+                      interleaved, n_stride, q, k, v, q_obs, stream, check=True) -> int:
+    rc = lib().arkv_qk_norm_rope(_ref(cfg), n_tok, qkv, qkv_stride, pos0, step, length, q_weight, k_weight,
+                                 eps, freq, rot, interleaved, n_stride, q, k, v, q_obs, stream)
+    return _check("arkv_qk_norm_rope", rc) if check else rc
+
+
+def arkv_cache_fork(dst_cfg, dst, src_cfg, src, src_seq, stream, check=True) -> int:
+    rc = lib().arkv_cache_fork(_ref(dst_cfg), _ref(dst), _ref(src_cfg), _ref(src), src_seq, stream)
+    return _check("arkv_cache_fork", rc) if check else rc
+
+
+def arkv_prefix_workspace_bytes(cfg: arkv_cfg, prefix_cfg: arkv_cfg) -> int:
+    return lib().arkv_prefix_workspace_bytes(_ref(cfg), _ref(prefix_cfg))
+
+
+def arkv_prefix_attn(cfg, prefix_cfg, q, prefix, branch_start, o_own, ml_own, o, ml, ws, ws_bytes, stream,
+                     check=True) -> int:
+    rc = lib().arkv_prefix_attn(_ref(cfg), _ref(prefix_cfg), q, _ref(prefix), branch_start, o_own, ml_own, o,
+                                ml, ws, ws_bytes, stream)
+    return _check("arkv_prefix_attn", rc) if check else rc
+
+
+def arkv_decode_ml(cfg, ws, ws_bytes) -> int:
+    """Address of the heads' (max, sum) in a decode workspace."""
+    out = ctypes.c_void_p()
+    _check("arkv_decode_ml", lib().arkv_decode_ml(_ref(cfg), ws, ws_bytes, ctypes.byref(out)))
+    return out.value

@@ -1,6 +1,8 @@
 """Device-memory plumbing around libarkv: torch tensors for one layer's packed
-cache and workspaces, and a per-layer driver that issues the C-ABI calls of the
-decode path in order.  Nothing here computes any part of the method.
+cache and workspaces, and per-layer drivers that issue the C-ABI calls of the
+decode path in order: a sequence's own step, a step of branches that share a
+prefix, forks of a cache, and the projection's norm and rotation before them.
+Nothing here computes any part of the method.
 """
 from __future__ import annotations
 
@@ -94,3 +96,96 @@ def decode_step(st: LayerState, step: int, q, k_new, v_new, ctx_len, o, reassign
         abi.arkv_reassign(st.cfg, step, st.r, ctx_len.data_ptr(), st.cache.c,
                           tier_dbg.data_ptr() if tier_dbg is not None else None,
                           st.ws_reassign.ptr, st.ws_reassign.nbytes, s)
+
+
+def _on_device(t: torch.Tensor, stream):
+    """The device guard and raw stream of a call on t's device."""
+    s = stream if stream is not None else torch.cuda.current_stream(t.device)
+    return torch.cuda.device(t.device), s.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rope_frequencies(rot: int, theta: float, device) -> torch.Tensor:
+    """theta ** (-2 i / rot) for the rot / 2 rotated pairs, float64 radians per position."""
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    return (float(theta) ** (-2.0 * i / max(rot, 1))).to(device)
+
+
+def qk_norm_rope(cfg: abi.arkv_cfg, qkv, n_tok: int, freq, k, v, q=None, q_obs=None, *, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, interleaved=False, pos0=None, step: int = 0, length=None,
+                 stream=None):
+    """arkv_qk_norm_rope on torch tensors: qkv [batch * n_tok, >= (hq + 2 hkv) D] bf16 (unit stride in
+    its last dimension), freq [rot / 2] float64 or None, k, v (and q) [batch, heads, n, D] bf16."""
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.shape[0] != cfg.batch * n_tok:
+        raise ValueError("qkv must be [batch * n_tok, width] with unit stride in its last dimension")
+    for name, t, heads in (("q", q, cfg.hq), ("k", k, cfg.hkv), ("v", v, cfg.hkv), ("q_obs", q_obs, cfg.hq)):
+        if t is None and name in ("q", "q_obs"):
+            continue
+        n = cfg.n_obs if name == "q_obs" else k.shape[2]
+        if not t.is_contiguous() or tuple(t.shape) != (cfg.batch, heads, n, cfg.head_dim):
+            raise ValueError(f"{name} must be a contiguous [batch, heads, n, head_dim] tensor")
+    for name, t, dt in (("qkv", qkv, torch.bfloat16), ("q", q, torch.bfloat16), ("k", k, torch.bfloat16),
+                        ("v", v, torch.bfloat16), ("q_obs", q_obs, torch.bfloat16),
+                        ("q_weight", q_weight, torch.bfloat16), ("k_weight", k_weight, torch.bfloat16),
+                        ("freq", freq, torch.float64), ("pos0", pos0, torch.int32), ("length", length, torch.int32)):
+        if t is not None and (t.dtype != dt or t.device != qkv.device):
+            raise ValueError(f"{name} must be {dt} on {qkv.device}")
+    guard, s = _on_device(qkv, stream)
+    with guard:
+        abi.arkv_qk_norm_rope(cfg, n_tok, qkv.data_ptr(), qkv.stride(0), _ptr(pos0), step, _ptr(length),
+                              _ptr(q_weight), _ptr(k_weight), eps, _ptr(freq), 0 if freq is None else 2 * freq.numel(),
+                              int(bool(interleaved)), k.shape[2], _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_obs), s)
+
+
+def fork(dst: LayerCache, src: LayerCache, src_seq, stream=None):
+    """arkv_cache_fork: sequence b of dst becomes a copy of sequence src_seq[b] of src (int32 tensor;
+    abi.ARKV_SEQ_FREE, abi.ARKV_SEQ_KEEP).  dst may be src itself (see include/arkv.h)."""
+    if src_seq.dtype != torch.int32 or src_seq.numel() != dst.cfg.batch or not src_seq.is_contiguous():
+        raise ValueError("src_seq must be a contiguous int32 tensor with one entry per sequence of dst")
+    if not (src_seq.device == dst.k16.device == src.k16.device):
+        raise ValueError("src_seq and the two caches must be on one device")
+    guard, s = _on_device(dst.k16, stream)
+    with guard:
+        abi.arkv_cache_fork(dst.cfg, dst.c, src.cfg, src.c, src_seq.data_ptr(), s)
+
+
+@dataclass
+class SharedPrefix:
+    """A packed cache whose sequences are prefixes, shared by the branches of another layer state."""
+    cache: LayerCache
+    branch_start: torch.Tensor | None    # [prefixes + 1] int32, or None: one prefix, every branch
+    ws: Workspace
+
+
+def new_shared_prefix(branches: abi.arkv_cfg, cache: LayerCache, branch_start=None) -> SharedPrefix:
+    """The prefixes in `cache` for the branches described by `branches`."""
+    dev = cache.k16.device
+    if branch_start is not None:
+        branch_start = torch.as_tensor(branch_start, dtype=torch.int32, device=dev).contiguous()
+        if branch_start.numel() != cache.cfg.batch + 1:
+            raise ValueError("branch_start must have one entry per prefix and one more")
+    return SharedPrefix(cache, branch_start,
+                        Workspace(abi.arkv_prefix_workspace_bytes(branches, cache.cfg), dev))
+
+
+def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new, ctx_len, o_own, o,
+                reassign_interval: int, stream=None, tier_dbg=None):
+    """One decode step of one layer whose sequences share prefixes: append + attend to the own
+    tokens (o_own, float32), attend to the prefix and join (o, bf16, and the heads' (max, sum) in
+    the decode workspace), score update of the own tokens, and their reassignment when
+    (step + 1) % reassign_interval == 0.  ctx_len counts the prefix's tokens."""
+    guard, s = _on_device(q, stream)
+    with guard:
+        abi.arkv_decode_attn(st.cfg, step, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), ctx_len.data_ptr(),
+                             st.cache.c, o_own.data_ptr(), st.ws_decode.ptr, st.ws_decode.nbytes, s)
+        ml = abi.arkv_decode_ml(st.cfg, st.ws_decode.ptr, st.ws_decode.nbytes)
+        abi.arkv_prefix_attn(st.cfg, prefix.cache.cfg, q.data_ptr(), prefix.cache.c, _ptr(prefix.branch_start),
+                             o_own.data_ptr(), ml, o.data_ptr(), ml, prefix.ws.ptr, prefix.ws.nbytes, s)
+        abi.arkv_score_update(st.cfg, step, ctx_len.data_ptr(), st.cache.c, st.ws_decode.ptr,
+                              st.ws_decode.nbytes, s)
+        if (step + 1) % reassign_interval == 0:
+            abi.arkv_reassign(st.cfg, step, st.r, ctx_len.data_ptr(), st.cache.c, _ptr(tier_dbg),
+                              st.ws_reassign.ptr, st.ws_reassign.nbytes, s)

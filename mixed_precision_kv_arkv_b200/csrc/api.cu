@@ -276,6 +276,113 @@ int arkv_copy_async(void* dst, const void* src, size_t bytes, arkv_stream_t stre
     return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_copy_async");
 }
 
+int arkv_qk_norm_rope(const arkv_cfg* cfg, int32_t n_tok, const uint16_t* qkv, int64_t qkv_stride,
+                      const int32_t* pos0, int32_t step, const int32_t* length, const uint16_t* q_weight,
+                      const uint16_t* k_weight, float eps, const double* freq, int32_t rot, int32_t interleaved,
+                      int32_t n_stride, uint16_t* q, uint16_t* k, uint16_t* v, uint16_t* q_obs,
+                      arkv_stream_t stream) {
+    ARKV_TRY(check_cfg(cfg));
+    if (!qkv || !k || !v) return fail(ARKV_EINVAL, "%s: null argument", "arkv_qk_norm_rope");
+    if (n_tok < 1 || n_stride < n_tok || step < 0)
+        return fail(ARKV_EINVAL, "%s: need n_tok >= 1, n_stride >= n_tok and step >= 0", "arkv_qk_norm_rope");
+    if (qkv_stride < (int64_t)(cfg->hq + 2 * (int64_t)cfg->hkv) * cfg->head_dim || qkv_stride % 8)
+        return fail(ARKV_EINVAL, "%s: qkv_stride must be a multiple of 8 and hold hq + 2 hkv heads", "arkv_qk_norm_rope");
+    if (rot < 0 || rot > cfg->head_dim || rot % 2 || (rot > 0 && !freq))
+        return fail(ARKV_EINVAL, "%s: rot must be even, in 0..head_dim, with its frequencies", "arkv_qk_norm_rope");
+    if (interleaved != 0 && interleaved != 1) return fail(ARKV_EINVAL, "%s: interleaved must be 0 or 1", "arkv_qk_norm_rope");
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(ARKV_EINVAL, "%s: eps must be finite and >= 0", "arkv_qk_norm_rope");
+    const void* rows[] = {qkv, q, k, v, q_obs};
+    for (const void* x : rows)
+        if (!aligned(x, 16)) return fail(ARKV_EINVAL, "%s: qkv and the outputs must be 16-byte aligned", "arkv_qk_norm_rope");
+    if (!aligned(q_weight, 2) || !aligned(k_weight, 2) || !aligned(freq, 8) || !aligned(pos0, 4) || !aligned(length, 4))
+        return fail(ARKV_EINVAL, "%s: a misaligned argument", "arkv_qk_norm_rope");
+    if ((int64_t)cfg->batch * n_tok > INT_MAX)
+        return fail(ARKV_EINVAL, "%s: batch * n_tok must fit in 31 bits", "arkv_qk_norm_rope");
+    arkv::RopeParams p{};
+    p.d = dims(cfg); p.n_tok = n_tok; p.step = step; p.rot = rot; p.interleaved = interleaved; p.n_stride = n_stride;
+    p.qkv_stride = qkv_stride; p.qkv = qkv; p.pos0 = pos0; p.length = length;
+    p.q_weight = q_weight; p.k_weight = k_weight; p.eps = eps; p.freq = freq;
+    p.q = q; p.k = k; p.v = v; p.q_obs = q_obs;
+    const cudaError_t e = arkv::launch_qk_norm_rope(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_qk_norm_rope");
+}
+
+int arkv_cache_fork(const arkv_cfg* dst_cfg, arkv_layer_cache* dst, const arkv_cfg* src_cfg,
+                    const arkv_layer_cache* src, const int32_t* src_seq, arkv_stream_t stream) {
+    ARKV_TRY(check_cfg(dst_cfg));
+    ARKV_TRY(check_cfg(src_cfg));
+    ARKV_TRY(check_cache(dst));
+    ARKV_TRY(check_cache(src));
+    if (!src_seq || !aligned(src_seq, 4)) return fail(ARKV_EINVAL, "%s: src_seq is null or misaligned", "arkv_cache_fork");
+    if (dst_cfg->hkv != src_cfg->hkv || dst_cfg->head_dim != src_cfg->head_dim ||
+        dst_cfg->quant_format != src_cfg->quant_format)
+        return fail(ARKV_EINVAL, "%s: hkv, head_dim and quant_format of the two caches differ", "arkv_cache_fork");
+    // one cache or two: every buffer the same (and the shapes with it), or none
+    const void* a[] = {dst->k16, dst->v16, dst->pos16, dst->mu16, dst->m2_16, dst->k8, dst->v8, dst->sk, dst->sv,
+                       dst->pos8, dst->mu8, dst->m2_8, dst->n_bf16, dst->n_fp8};
+    const void* b[] = {src->k16, src->v16, src->pos16, src->mu16, src->m2_16, src->k8, src->v8, src->sk, src->sv,
+                       src->pos8, src->mu8, src->m2_8, src->n_bf16, src->n_fp8};
+    int same = 0;
+    for (int i = 0; i < 14; ++i) same += a[i] == b[i];
+    if (same != 0 && (same != 14 || dst_cfg->batch != src_cfg->batch || dst_cfg->cap_bf16 != src_cfg->cap_bf16 ||
+                      dst_cfg->cap_fp8 != src_cfg->cap_fp8))
+        return fail(ARKV_EINVAL, "%s: dst and src must be one cache or share no buffer", "arkv_cache_fork");
+    arkv::ForkParams p{};
+    p.D = dst_cfg->head_dim; p.hkv = dst_cfg->hkv; p.dst_batch = dst_cfg->batch; p.src_batch = src_cfg->batch;
+    p.dst_cap_o = dst_cfg->cap_bf16; p.dst_cap_q = dst_cfg->cap_fp8;
+    p.src_cap_o = src_cfg->cap_bf16; p.src_cap_q = src_cfg->cap_fp8;
+    p.in_place = same != 0; p.src_seq = src_seq; p.dst = *dst; p.src = *src;
+    const cudaError_t e = arkv::launch_cache_fork(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_cache_fork");
+}
+
+static int check_prefix_cfg(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg) {
+    ARKV_TRY(check_cfg(cfg));
+    ARKV_TRY(check_cfg(prefix_cfg));
+    if (cfg->hq != prefix_cfg->hq || cfg->hkv != prefix_cfg->hkv || cfg->head_dim != prefix_cfg->head_dim)
+        return fail(ARKV_EINVAL, "%s: hq, hkv and head_dim of the branches and the prefixes differ", "arkv_prefix_attn");
+    return ARKV_OK;
+}
+
+size_t arkv_prefix_workspace_bytes(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg) {
+    if (check_prefix_cfg(cfg, prefix_cfg) != ARKV_OK) return 0;
+    return arkv::prefix_ws_bytes(dims(prefix_cfg), cfg->batch);
+}
+
+int arkv_prefix_attn(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, const uint16_t* q, const arkv_layer_cache* prefix,
+                     const int32_t* branch_start, const float* o_own, const float* ml_own, uint16_t* o, float* ml,
+                     void* ws, size_t ws_bytes, arkv_stream_t stream) {
+    ARKV_TRY(check_prefix_cfg(cfg, prefix_cfg));
+    ARKV_TRY(check_cache(prefix));
+    if (!q || !o) return fail(ARKV_EINVAL, "%s: null argument", "arkv_prefix_attn");
+    if (!branch_start && prefix_cfg->batch != 1)
+        return fail(ARKV_EINVAL, "%s: several prefixes need branch_start", "arkv_prefix_attn");
+    if (!o_own != !ml_own) return fail(ARKV_EINVAL, "%s: o_own and ml_own go together", "arkv_prefix_attn");
+    if (!aligned(q, 16) || !aligned(o_own, 16) || !aligned(o, 16) || !aligned(ml_own, 8) || !aligned(ml, 8) ||
+        !aligned(branch_start, 4))
+        return fail(ARKV_EINVAL, "%s: q, o_own and o must be 16-byte, ml 8-byte aligned", "arkv_prefix_attn");
+    const arkv::LayerDims d = dims(prefix_cfg);
+    if ((int64_t)d.R * d.cap_o > INT_MAX - 256 || (int64_t)d.R * d.cap_q > INT_MAX - 256)
+        return fail(ARKV_EINVAL, "%s: prefix rows times capacity must fit in 31 bits", "arkv_prefix_attn");
+    ARKV_TRY(check_ws(ws, ws_bytes, arkv::prefix_ws_bytes(d, cfg->batch)));
+    arkv::PrefixParams p{};
+    p.d = d; p.branches = cfg->batch; p.q = q; p.c = *prefix; p.branch_start = branch_start;
+    p.o_own = o_own; p.ml_own = (const float2*)ml_own; p.o = o; p.ml = (float2*)ml;
+    p.inv_sqrt_d = 1.0 / sqrt((double)d.D);
+    p.early_start = cfg->early_start;
+    const cudaError_t e = arkv::launch_prefix_attn(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_prefix_attn");
+}
+
+int arkv_decode_ml(const arkv_cfg* cfg, void* ws, size_t ws_bytes, float** ml) {
+    ARKV_TRY(check_cfg(cfg));
+    if (!ml) return fail(ARKV_EINVAL, "%s: null argument", "arkv_decode_ml");
+    const arkv::DecodeWs w = arkv::decode_ws_layout(dims(cfg));
+    ARKV_TRY(check_ws(ws, ws_bytes, w.total));
+    *ml = (float*)((char*)ws + w.ml);
+    return ARKV_OK;
+}
+
 int arkv_fp8_encode(int32_t format, const float* x, uint8_t* out, size_t n, arkv_stream_t stream) {
     if (format != ARKV_FMT_E4M3 && format != ARKV_FMT_E5M2)
         return fail(ARKV_EINVAL, "%s: unknown format", "arkv_fp8_encode");

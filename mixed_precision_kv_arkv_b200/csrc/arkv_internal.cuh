@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -216,6 +217,46 @@ struct PrefillWs {
 };
 PrefillWs prefill_ws_layout(const LayerDims& d, int n_stride);
 cudaError_t launch_prefill_stats(const PrefillParams& p, cudaStream_t s);
+
+struct RopeParams {
+    LayerDims d;
+    int n_tok, step, rot, interleaved, n_stride;
+    int64_t qkv_stride;
+    const uint16_t* qkv;
+    const int32_t* pos0;       // nullable
+    const int32_t* length;     // nullable
+    const uint16_t* q_weight;  // nullable
+    const uint16_t* k_weight;  // nullable
+    float eps;
+    const double* freq;
+    uint16_t *q, *k, *v, *q_obs;   // q, q_obs nullable
+};
+cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s);
+
+struct ForkParams {
+    int D, hkv, dst_batch, src_batch;
+    int dst_cap_o, dst_cap_q, src_cap_o, src_cap_q;
+    int in_place;
+    const int32_t* src_seq;
+    arkv_layer_cache dst, src;
+};
+cudaError_t launch_cache_fork(const ForkParams& p, cudaStream_t s);
+
+struct PrefixParams {
+    LayerDims d;    // the prefixes (R = prefixes * hkv rows)
+    int branches;
+    const uint16_t* q;
+    arkv_layer_cache c;
+    const int32_t* branch_start;   // nullable: one prefix, every branch
+    const float* o_own;            // nullable
+    const float2* ml_own;          // nullable
+    uint16_t* o;
+    float2* ml;                    // nullable
+    double inv_sqrt_d;
+    int early_start;
+};
+size_t prefix_ws_bytes(const LayerDims& d, int branches);
+cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t s);
 
 cudaError_t launch_fp8_encode(int fmt, const float* x, uint8_t* out, size_t n, cudaStream_t s);
 
