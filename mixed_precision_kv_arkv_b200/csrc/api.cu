@@ -370,7 +370,7 @@ int arkv_prefix_attn(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, const uint
     p.o_own = o_own; p.ml_own = (const float2*)ml_own; p.o = o; p.ml = (float2*)ml;
     p.inv_sqrt_d = 1.0 / sqrt((double)d.D);
     p.early_start = cfg->early_start;
-    const cudaError_t e = arkv::launch_prefix_attn(p, (cudaStream_t)stream);
+    const cudaError_t e = arkv::launch_prefix_attn(p, ws, (cudaStream_t)stream);
     return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_prefix_attn");
 }
 

@@ -256,7 +256,7 @@ struct PrefixParams {
     int early_start;
 };
 size_t prefix_ws_bytes(const LayerDims& d, int branches);
-cudaError_t launch_prefix_attn(const PrefixParams& p, cudaStream_t s);
+cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s);
 
 cudaError_t launch_fp8_encode(int fmt, const float* x, uint8_t* out, size_t n, cudaStream_t s);
 
