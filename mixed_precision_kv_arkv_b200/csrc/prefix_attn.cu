@@ -2,26 +2,33 @@
 // joined with each branch's own part.
 //
 // The queries of a prefix's branches that meet the same key head are the rows of one
-// matrix (row = branch x query of the group, 128 rows a tile), so the prefix is read
+// matrix (row = branch x query of the group, tiles of 128 rows), so the prefix is read
 // once for all of them and both products run on the tensor cores:
 //   S[128 rows][128 tokens] = Q K^T,   O[128 rows][D] += P V,   P = 2^(S c - m).
 //
-// Work.  A unit is (prefix, key head, tile of rows); its tiles of 128 tokens are the
-// bf16 and the FP8 tiles of the prefix row, interleaved evenly, because an FP8 tile has
-// twice the arithmetic per byte.  The tiles of all units form one list, cut into equal
-// runs, one a CTA and one CTA an SM; a run that crosses units is several segments, each
-// with a partial (max, sum, unnormalised o) of its own in the workspace.
+// Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 128 tokens
+// are the bf16 and the FP8 tiles of the prefix row, interleaved evenly, because an FP8
+// tile has twice the arithmetic per byte.  The tiles of all units form one list, cut into
+// equal runs, one a CTA and one CTA an SM; a run that crosses units is several segments,
+// each with a partial (max, sum, unnormalised o) in the workspace.  In the list every unit
+// begins with kSegCost empty places, about what the start of another segment costs, so
+// that the run that holds them has that many tiles less.
 // prefix_join_kernel joins the partials and the branch's own part.
 //
 // A CTA: warp 0 streams K and V by TMA through a ring of slots (a slot is a tile's K or
-// its V), warp 1 issues the products, two warpgroups take the tiles in turn (softmax;
-// thread = row = tensor-memory lane), each with its own S, P and O in tensor memory and
-// its own softmax state, so that neither waits for the other, and one warpgroup rewrites
-// FP8 tiles in place as bf16 (exact: 4 or 3 significant bits).  P takes the place of S.
-// The K scale of an FP8 token enters the exponent's factor, its V scale is folded into P.
-// The softmax reference m moves only when a logit exceeds it by 2^8, so O is seldom
-// rescaled.  P is rounded to bf16 once, the rounding that o itself gets; the sum is of
-// the unrounded values.
+// its V), warp 1 issues the products, two warpgroups do the softmax (thread = row =
+// tensor-memory lane), each with its own S, P and O in tensor memory and its own state, so
+// that neither waits for the other, and two warpgroups rewrite FP8 tiles in place as bf16
+// (exact: 4 or 3 significant bits), one K, one V.  With one tile of rows the softmax
+// warpgroups take the token tiles in turn and their two O are added at the end of the
+// segment; with two each has its rows, and a token tile is loaded and converted once for
+// both.  Either way a softmax job is one S, and the jobs alternate.
+// P takes the place of S.  The K scale of an FP8 token enters the exponent's factor, its V
+// scale is folded into P.  The softmax reference m moves only when a logit exceeds it by
+// 2^8, so O is seldom rescaled.  P is rounded to bf16 once, the rounding that o itself
+// gets; the sum is of the unrounded values.
+// The loops over a tile's columns are not unrolled past 32: a short call runs each piece of
+// code once or twice, and fetching it cost more than the arithmetic.
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
 // memory is freed and the call ends.
@@ -41,35 +48,49 @@ using namespace tc;
 
 constexpr float kNegInf = -INFINITY;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kRows = 128;            // query rows of a unit
+constexpr int kRows = 128;            // query rows of a tile
 constexpr int kTok = 128;             // tokens of a tile
-constexpr int kThreads = 512;
+constexpr int kWarps = 20;            // 4 of single roles, 2 x 4 softmax, 2 x 4 conversion
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;         // of one call
+constexpr int kSegCost = 3;           // a segment's start and end, in tiles
 constexpr int kSpinLimit = 1 << 20;   // polls of one wait
+
+struct RowInfo {
+    int n16, n8, T16, T8, b0, nb, mt;   // live slots, tiles, first branch, branches, units
+};
+
+// This CTA's run of the list: [v, v_end); the row that holds place v, its first place, the
+// units before it.
+struct Sched {
+    int v, v_end, base, row, units;
+    RowInfo r;
+};
 
 // ------------------------------------------------------------------ shared memory
 template <int D>
 struct Smem {
-    static constexpr int kSlots = 6;                        // three tiles in flight
+    static constexpr int kSlots = 5;
     static constexpr int kSlot = kTok * D * 2;              // a K or V tile in bf16
     static constexpr int kRegion = kTok * 128;              // 64 dimensions of it (128-byte rows, swizzled)
     static constexpr int kRaw = D == 64 ? kSlot / 2 : 0;    // where in its slot an FP8 tile lands
-    static constexpr int kQ = 0;
-    static constexpr int kRing = kRows * D * 2;
+    static constexpr int kQ = 0;                            // two tiles of queries
+    static constexpr int kQTile = kRows * D * 2;
+    static constexpr int kRing = 2 * kQTile;
     static constexpr int kScale = kRing + kSlots * kSlot;   // float [2][2][kTok]: K (log2 units) and V scales
     static constexpr int kBars = kScale + 2 * 2 * kTok * 4;
-    // mbarriers.  A slot's load completes on kFullB, or on kRawB if the tile has to be
-    // converted first (kConvB tells when): each barrier then has one reader that sees every
-    // one of its phases, whichever kinds of tile come in between.
-    static constexpr int kFullB = 0, kEmptyB = kSlots, kRawB = 2 * kSlots, kConvB = 3 * kSlots, kQFull = 4 * kSlots,
+    // mbarriers.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
+    // the tile has to be converted first (kConvB tells when): each barrier then has one
+    // reader that sees every one of its phases, whichever kinds of tile come in between.
+    static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
                          kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 2, kScFull = kPFull + 2,
                          kScFree = kScFull + 2, kOFull = kScFree + 2, kXch = kOFull + 1, kEpi = kXch + 1,
-                         kFin = kEpi + 1, kCvt = kFin + 1, kNumBars = kCvt + 1;
+                         kFin = kEpi + 1, kCvt = kFin + 1, kNumBars = kCvt + 2;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
-    static constexpr int kSched = kMisc + 16;                           // this CTA's run
-    static constexpr int kSums = kSched + 32;                           // longlong2 [16]: the scan's warp sums
-    static constexpr int kBytes = kSums + 16 * 16;
-    static_assert(kBytes <= 232448, "shared memory of one CTA");
+    static constexpr int kSched = kMisc + 16;
+    static constexpr int kSums = kSched + 64;                           // int2 [kWarps]: the scan's warp sums
+    static constexpr int kBytes = kSums + kWarps * 8;
+    static_assert(sizeof(Sched) <= 64 && kBytes <= 232448, "shared memory of one CTA");
 };
 
 // tensor-memory columns: S (and P) of the two warpgroups, then their O
@@ -83,86 +104,105 @@ struct AttnArgs {
     CUtensorMap tm_q;                       // [branches][hkv][G][D] bf16, boxes of 128 / G branches x G x 64
     CUtensorMap tm_k16, tm_v16, tm_k8, tm_v8;   // [R * cap][D], boxes of 128 tokens
     PrefixParams p;
-    float* part_o;       // [slots][128][D]
-    float2* part_ml;     // [slots][128]
-    longlong2* starts;   // [R + 1]: tiles and units before each row
+    float4* part_o;      // [slots][row_tiles][D / 4][128 rows]: a warp's rows side by side
+    float2* part_ml;     // [slots][row_tiles][128]
+    int2* starts;        // [R + 1]: list places and units before each row
     int slots;
-    int per_tile;        // branches of one unit
-};
-
-struct RowInfo {
-    int n16, n8, T16, T8, b0, nb, mt;   // live slots, tiles, first branch, branches, units
+    int per_tile;        // branches of one tile of rows
+    int row_tiles;       // tiles of rows of a unit, at most
 };
 
 __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int row) {
     const LayerDims& d = a.p.d;
     RowInfo r;
     const int pre = row / d.hkv;
+    r.n16 = __ldg(a.p.c.n_bf16 + row);
+    r.n8 = __ldg(a.p.c.n_fp8 + row);
     int b0 = 0, b1 = a.p.branches;
     if (a.p.branch_start) {
-        b0 = min(max(__ldg(a.p.branch_start + pre), 0), b1);
-        b1 = min(max(__ldg(a.p.branch_start + pre + 1), b0), b1);
+        const int s0 = __ldg(a.p.branch_start + pre), s1 = __ldg(a.p.branch_start + pre + 1);
+        b0 = min(max(s0, 0), b1);
+        b1 = min(max(s1, b0), b1);
     }
     r.b0 = b0;
     r.nb = b1 - b0;
-    r.mt = (r.nb + a.per_tile - 1) / a.per_tile;
-    r.n16 = min(max(__ldg(a.p.c.n_bf16 + row), 0), d.cap_o);   // clamped to the capacities
-    r.n8 = min(max(__ldg(a.p.c.n_fp8 + row), 0), d.cap_q);
+    r.mt = (r.nb + a.row_tiles * a.per_tile - 1) / (a.row_tiles * a.per_tile);
+    r.n16 = min(max(r.n16, 0), d.cap_o);   // clamped to the capacities
+    r.n8 = min(max(r.n8, 0), d.cap_q);
     r.T16 = (r.n16 + kTok - 1) / kTok;
     r.T8 = (r.n8 + kTok - 1) / kTok;
     return r;
 }
+// Places a unit of this row takes in the list.
+__device__ __forceinline__ int unit_len(const RowInfo& r) { return r.T16 + r.T8 > 0 ? r.T16 + r.T8 + kSegCost : 0; }
 
-// Run of CTA c of P over T tiles: [c T / P, (c + 1) T / P); the CTA of tile t.
-__device__ __forceinline__ long long run_begin(long long T, int P, int c) { return T * c / P; }
-__device__ __forceinline__ int run_of(long long T, int P, long long t) { return (int)(((t + 1) * P + T - 1) / T) - 1; }
-
-struct Sched {
-    long long t, t_end, base;   // this CTA's run; tiles before `row`
-    int row, units;             // the row that holds tile t; units before it
+// Run c of P over V places begins at c V / P (V = q P + r, so the product stays small).
+struct Runs {
+    int V, P, q, r;
+    __device__ __forceinline__ Runs(int total, int ctas) : V(total), P(min(ctas, total)) {
+        q = P > 0 ? V / P : 0;
+        r = V - q * P;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * q + c * r / P; }
+    __device__ __forceinline__ int of(int v) const {   // the run that holds place v
+        int c = min((int)((float)v / (float)V * (float)P), P - 1);
+        while (c > 0 && begin(c) > v) --c;
+        while (begin(c + 1) <= v) ++c;
+        return c;
+    }
 };
 
 struct Tile {
     int fp8, idx, valid;   // kind, place in its segment, live tokens
 };
 
-// Walks a CTA's run: segments (the run's part of one unit), then their tiles.
+// Walks a CTA's run: segments (the run's tiles of one unit), then their tiles.
 struct Walk {
     const AttnArgs& a;
-    long long t, t_end, base;   // next tile, end of the run, first tile of the unit
-    int row, m, unit0;          // the unit: row, tile of rows; units before the row
+    int v, v_end, base;         // next place, end of the run, first place of the unit
+    int row, m, unit0;          // the unit: row, place in it; units before the row
     RowInfo r;
     int T, i, i_end, err, f8;   // tiles of the unit; next tile and end of the segment; the interleave
 
     __device__ __forceinline__ Walk(const AttnArgs& args, const Sched& s)
-        : a(args), t(s.t), t_end(s.t_end), base(s.base), row(s.row), m(0), unit0(s.units), r(row_info(args, s.row)),
-          T(r.T16 + r.T8), i(0), i_end(0), err(0), f8(0) {
+        : a(args), v(s.v), v_end(s.v_end), base(s.base), row(s.row), m(0), unit0(s.units), r(s.r), T(r.T16 + r.T8), i(0),
+          i_end(0), err(0), f8(0) {
         if (T > 0) {
-            m = (int)((t - base) / T);
-            base += (long long)m * T;
+            m = (v - base) / (T + kSegCost);
+            base += m * (T + kSegCost);
         }
     }
     __device__ __forceinline__ bool segment() {
-        if (t >= t_end) return false;
-        while (t >= base + T) {
-            base += T;
-            if (++m >= r.mt) {
-                do {
-                    unit0 += r.mt;
-                    if (++row >= a.p.d.R) return false;
-                    r = row_info(a, row);
-                    T = r.T16 + r.T8;
-                } while (T == 0 || r.mt == 0);
-                m = 0;
+        while (v < v_end) {
+            while (v >= base + T + kSegCost) {
+                base += T + kSegCost;
+                if (++m >= r.mt) {
+                    do {
+                        unit0 += r.mt;
+                        if (++row >= a.p.d.R) return false;
+                        r = row_info(a, row);
+                        T = r.T16 + r.T8;
+                    } while (T == 0 || r.mt == 0);
+                    m = 0;
+                }
+            }
+            i = max(v - base - kSegCost, 0);
+            i_end = min(v_end - base - kSegCost, T);
+            v = min(base + kSegCost + T, v_end);
+            if (i < i_end) {   // after i tiles, floor(i T8 / T) are FP8
+                if (T < 65536) {
+                    const unsigned w = (unsigned)i * r.T8;
+                    f8 = w / (unsigned)T;
+                    err = w - f8 * T;
+                } else {
+                    const long long w = (long long)i * r.T8;
+                    f8 = (int)(w / T);
+                    err = (int)(w - (long long)f8 * T);
+                }
+                return true;
             }
         }
-        i = (int)(t - base);
-        i_end = (int)min((long long)T, t_end - base);
-        const long long w = (long long)i * r.T8;   // after i tiles, floor(i T8 / T) are FP8
-        f8 = (int)(w / T);
-        err = (int)(w - (long long)f8 * T);
-        t = base + i_end;
-        return true;
+        return false;
     }
     __device__ __forceinline__ Tile tile() {
         Tile x;
@@ -179,6 +219,8 @@ struct Walk {
         ++i;
         return x;
     }
+    __device__ __forceinline__ int first_branch() const { return m * a.row_tiles * a.per_tile; }   // of the prefix's
+    __device__ __forceinline__ bool two() const { return r.nb - first_branch() > a.per_tile; }     // tiles of rows
 };
 
 // ------------------------------------------------------------------ helpers
@@ -239,19 +281,20 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w)
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     int e = 0, seg = 0;
-    uint32_t full = 0, raw = 0, last = 0;   // parity of each slot's next phase; which barrier its last load is on
+    uint32_t ph[3] = {0, 0, 0}, last[3] = {0, 0, 0};   // by barrier (full, raw K, raw V): parity of each slot's next
+                                                       // phase, the slots whose last load it has
     bool ok = true, waited = !a.p.early_start;
     auto load = [&](const Tile& x, bool v) {
         const int s = e % L::kSlots;
         if (e >= L::kSlots && !cx.wait(L::kEmptyB + s, ((e / L::kSlots) & 1) ^ 1)) return false;
         const bool conv = x.fp8 || (v && x.valid < kTok);
-        const uint32_t dst = smem + L::kRing + s * L::kSlot, bar = cx.bar((conv ? L::kRawB : L::kFullB) + s);
-        if (conv) {
-            raw ^= 1u << s;
-            last |= 1u << s;
-        } else {
-            full ^= 1u << s;
-            last &= ~(1u << s);
+        const int kind = conv ? (v ? 2 : 1) : 0;
+        const uint32_t dst = smem + L::kRing + s * L::kSlot;
+        const uint32_t bar = cx.bar((kind == 0 ? L::kFullB : kind == 1 ? L::kRawB : L::kRawB + L::kSlots) + s);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            if (i == kind) ph[i] ^= 1u << s;
+            last[i] = i == kind ? last[i] | (1u << s) : last[i] & ~(1u << s);
         }
         if (x.fp8) {
             mbar_expect_tx(bar, kTok * D);
@@ -279,33 +322,40 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w)
                 waited = true;
             }
             if (seg > 0 && !(ok = cx.wait(L::kQEmpty, (seg - 1) & 1))) continue;
-            mbar_expect_tx(cx.bar(L::kQFull), a.per_tile * d.G * D * 2);
+            const int tiles = w.two() ? 2 : 1, b0 = w.r.b0 + w.first_branch();
+            mbar_expect_tx(cx.bar(L::kQFull), tiles * a.per_tile * d.G * D * 2);
+            for (int t = 0; t < tiles; ++t)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(smem + L::kQ + c * L::kRegion, &a.tm_q, 64 * c, 0, w.row % d.hkv, w.r.b0 + w.m * a.per_tile,
-                            cx.bar(L::kQFull));
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem + L::kQ + t * L::kQTile + c * L::kRegion, &a.tm_q, 64 * c, 0, w.row % d.hkv,
+                                b0 + t * a.per_tile, cx.bar(L::kQFull));
             ++seg;
         }
     }
     // copies in flight land before the CTA ends, also when it gives up
-    for (int s = 0; s < min(e, L::kSlots); ++s) {
-        const bool r = (last >> s) & 1u;
-        const uint32_t par = (((r ? raw : full) >> s) & 1u) ^ 1u;
-        for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar((r ? L::kRawB : L::kFullB) + s), par); ++z) {
-        }
-    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        for (int s = 0; s < L::kSlots; ++s)
+            if ((last[i] >> s) & 1u)
+                for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar((i == 0 ? L::kFullB : i == 1 ? L::kRawB : L::kRawB + L::kSlots) + s),
+                                                                 ((ph[i] >> s) & 1u) ^ 1u); ++z) {
+                }
     if (seg > 0)
         for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kQFull), (seg - 1) & 1); ++z) {
         }
 }
 
 // ------------------------------------------------------------------ products (one thread)
+// Softmax job x of a segment belongs to warpgroup x & 1: token tile x with one tile of
+// rows, token tile x / 2 with two.  S of job x + 1 is issued before P V of job x, and so
+// after that of job x - 1, which read P from the same place.
 template <int D>
 __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32_t tmem, Walk w) {
     using L = Smem<D>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false), kIdPV = idesc_bf16(kRows, D, true);
-    int j = 0, seg = 0;        // tiles and segments so far
+    int j = 0, seg = 0;            // tiles and segments so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
+    uint32_t p_ph = 0;             // parity of each warpgroup's next P
     bool ok = true;
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
     auto ready = [&](int e, bool converted) {   // entry e has landed (and been converted)
@@ -315,47 +365,50 @@ __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32
         ph ^= 1u << s;
         return r;
     };
-    auto qk = [&](const Tile& x, int jj, bool last) {
-        const int e = 2 * jj, s = e % L::kSlots, b = jj & 1;
-        if (!ready(e, x.fp8)) return false;
-        fence_after();
-        const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint64_t o = (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2);
-            mma_ss(tmem + tmem_s(b), q_desc + o, k_desc + o, kIdQK, k > 0);
-        }
-        commit(cx.bar(L::kSFull + b));
-        commit(cx.bar(L::kEmptyB + s));
-        if (last) commit(cx.bar(L::kQEmpty));
-        return true;
-    };
     while (ok && w.segment()) {
-        const int n = w.i_end - w.i;
+        const bool two = w.two();
+        const int sh = two ? 1 : 0, n = w.i_end - w.i, jobs = n << sh;
         ok = cx.wait(L::kQFull, seg & 1) && (seg == 0 || cx.wait(L::kEpi, (seg - 1) & 1));
-        if (!ok) break;
-        Tile cur = w.tile();
-        ok = qk(cur, j, n == 1);
-        bool started[2] = {false, false};
-        for (int x = 0; ok && x < n; ++x, ++j) {
-            Tile next = cur;
-            if (x + 1 < n) {
-                next = w.tile();
-                if (!(ok = qk(next, j + 1, x + 2 == n))) break;
-            }
-            const int e = 2 * j + 1, s = e % L::kSlots, b = j & 1;
-            if (!(ok = cx.wait(L::kPFull + b, (j >> 1) & 1) && ready(e, cur.fp8 || cur.valid < kTok))) break;
-            fence_after();
-            const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
+        uint32_t conv_v = 0;       // by job & 1: its V tile is converted
+        Tile t{};
+        for (int x = 0; ok && x <= jobs; ++x) {
+            if (x < jobs) {        // S of job x
+                const int b = x & 1, e = 2 * (j + (x >> sh)), s = e % L::kSlots;
+                const bool opens = !two || b == 0, closes = !two || b == 1;   // the tile's first, last job
+                if (opens) {
+                    t = w.tile();
+                    if (!(ok = ready(e, t.fp8))) break;
+                    fence_after();
+                }
+                conv_v = (conv_v & ~(1u << b)) | ((uint32_t)(t.fp8 || t.valid < kTok) << b);
+                const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
+                const uint64_t qd = q_desc + (uint64_t)(two ? b * (L::kQTile >> 4) : 0);
 #pragma unroll
-            for (int k = 0; k < kTok / 16; ++k)
-                mma_ts(tmem + tmem_o<D>(b), tmem + tmem_s(b) + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV,
-                       started[b] || k > 0);
-            started[b] = true;
-            commit(cx.bar(L::kEmptyB + s));
-            if (x + 1 == n) commit(cx.bar(L::kOFull));
-            cur = next;
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t o = (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2);
+                    mma_ss(tmem + tmem_s(b), qd + o, k_desc + o, kIdQK, k > 0);
+                }
+                commit(cx.bar(L::kSFull + b));
+                if (closes) commit(cx.bar(L::kEmptyB + s));
+                if (x + 1 == jobs) commit(cx.bar(L::kQEmpty));
+            }
+            if (x > 0) {           // P V of job x - 1
+                const int y = x - 1, b = y & 1, e = 2 * (j + (y >> sh)) + 1, s = e % L::kSlots;
+                const bool opens = !two || b == 0, closes = !two || b == 1;
+                if (!(ok = cx.wait(L::kPFull + b, (p_ph >> b) & 1u) && (!opens || ready(e, (conv_v >> b) & 1u)))) break;
+                p_ph ^= 1u << b;
+                fence_after();
+                const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
+                const bool add = y >= 2;   // each warpgroup's first product of the segment starts its O
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                    mma_ts(tmem + tmem_o<D>(b), tmem + tmem_s(b) + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV,
+                           add || k > 0);
+                if (closes) commit(cx.bar(L::kEmptyB + s));
+                if (x == jobs) commit(cx.bar(L::kOFull));
+            }
         }
+        j += n;
         ++seg;
     }
     // every product has completed before tensor memory is freed
@@ -365,88 +418,89 @@ __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32
 }
 
 // ------------------------------------------------------------------ FP8 -> bf16 (128 threads, one a token)
-template <int D, int FMT>
+// KV = 0: the K tiles and the scales, 1: the V tiles, whose rows past the segment end
+// become zero in either format (stale bits must not meet P = 0).
+template <int D, int FMT, int KV>
 __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, Walk w) {
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
     float* scales = reinterpret_cast<float*>(smem + L::kScale);
-    int cvt = 0;   // uses of the read-before-write barrier (D = 64)
-    uint32_t raw_ph = 0;             // parity of each slot's next phase
-    int uses[2] = {0, 0};            // FP8 tiles through each scale buffer
-    auto landed = [&](int s) {
-        const bool r = cx.warp_wait(L::kRawB + s, (raw_ph >> s) & 1u);
-        raw_ph ^= 1u << s;
-        return r;
-    };
-    auto rewrite = [&](int s, bool zero) {
-        char* slot = smem + L::kRing + s * L::kSlot;
-        uint4 raw[D / 16];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-            raw[c] = *reinterpret_cast<const uint4*>(slot + L::kRaw + (D == 128 ? sw128(ct, c) : sw64(ct, c)));
-        if (zero) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if constexpr (D == 64) {   // rows grow over other threads' codes (D = 128: over their own alone)
-            mbar_arrive(cx.bar(L::kCvt));
-            if (!cx.warp_wait(L::kCvt, cvt++ & 1)) return false;
-        }
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            uint4 lo, hi;
-            fp8x4_to_bf16<FMT>(raw[c].x, lo.x, lo.y);
-            fp8x4_to_bf16<FMT>(raw[c].y, lo.z, lo.w);
-            fp8x4_to_bf16<FMT>(raw[c].z, hi.x, hi.y);
-            fp8x4_to_bf16<FMT>(raw[c].w, hi.z, hi.w);
-            char* reg = slot + (c >> 2) * L::kRegion;
-            *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * (c & 3))) = lo;
-            *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * (c & 3) + 1)) = hi;
-        }
-        fence_proxy_async();
-        mbar_arrive(cx.bar(L::kConvB + s));
-        return true;
-    };
-    auto load_scales = [&](const Tile& x, int row, float& sk, float& sv) {
-        sk = sv = 0.f;   // zero past the segment end, where stale bits must not enter
-        if (x.fp8 && ct < x.valid) {
-            const size_t at = (size_t)row * d.cap_q + x.idx * kTok + ct;
-            sk = __ldg(a.p.c.sk + at);
-            sv = __ldg(a.p.c.sv + at);
-        }
-    };
+    int cvt = 0, f = 0;      // uses of the read-before-write barrier (D = 64); FP8 tiles so far
+    uint32_t raw_ph = 0;     // parity of each slot's next phase (of the K or V loads to convert)
     auto next = [&](Tile& x) {
         if (w.i == w.i_end && !w.segment()) return false;
         x = w.tile();
         return true;
     };
+    auto load_scales = [&](const Tile& x, int row, float& sk, float& sv) {
+        sk = 1.f;            // past the segment end: a masked column
+        sv = 0.f;
+        if (KV == 0 && x.fp8 && ct < x.valid) {
+            const size_t at = (size_t)row * d.cap_q + x.idx * kTok + ct;
+            sk = __ldg(a.p.c.sk + at) * c2;
+            sv = __ldg(a.p.c.sv + at);
+        }
+    };
     Tile cur{}, ahead{};
     float sk, sv, sk1 = 0.f, sv1 = 0.f;
     if (!next(cur)) return;
     load_scales(cur, w.row, sk, sv);
+#pragma unroll 1
     for (int j = 0;; ++j) {
         const bool more = next(ahead);   // the next tile's scales are loaded one tile early
         if (more) load_scales(ahead, w.row, sk1, sv1);
-        const int b = j & 1, ks = (2 * j) % L::kSlots, vs = (2 * j + 1) % L::kSlots;
-        if (cur.fp8) {
-            if (uses[b] > 0 && !cx.warp_wait(L::kScFree + b, (uses[b] - 1) & 1)) return;   // their last readers
-            ++uses[b];
-            scales[(2 * b) * kTok + ct] = sk * c2;
-            scales[(2 * b + 1) * kTok + ct] = sv;
-            mbar_arrive(cx.bar(L::kScFull + b));
-            if (!landed(ks) || !rewrite(ks, false)) return;
-            if (!landed(vs) || !rewrite(vs, ct >= cur.valid)) return;
-        } else if (cur.valid < kTok) {   // stale V rows past the end must not meet P = 0
-            if (!landed(vs)) return;
-            if (ct >= cur.valid) {
+        const int s = (2 * j + KV) % L::kSlots;
+        const bool tail = KV == 1 && !cur.fp8 && cur.valid < kTok;
+        if (cur.fp8 || tail) {
+            if (KV == 0) {
+                const int z = f & 1, use = f >> 1;
+                if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // their last readers
+                scales[(2 * z) * kTok + ct] = sk;
+                scales[(2 * z + 1) * kTok + ct] = sv;
+                mbar_arrive(cx.bar(L::kScFull + z));
+                ++f;
+            }
+            if (!cx.warp_wait(L::kRawB + KV * L::kSlots + s, (raw_ph >> s) & 1u)) return;
+            raw_ph ^= 1u << s;
+            char* slot = smem + L::kRing + s * L::kSlot;
+            const bool zero = KV == 1 && ct >= cur.valid;
+            if (!tail) {
+                // 64 dimensions at a time, the upper half of a 128-byte row first: the codes lie
+                // where the lower half goes
+#pragma unroll 1
+                for (int h = D / 64 - 1; h >= 0; --h) {
+                    uint4 raw[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        raw[c] = *reinterpret_cast<const uint4*>(
+                            slot + L::kRaw + (D == 128 ? sw128(ct, 4 * h + c) : sw64(ct, c)));
+                        if (zero) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if constexpr (D == 64) {   // rows grow over other threads' codes (D = 128: over their own alone)
+                        mbar_arrive(cx.bar(L::kCvt + KV));
+                        if (!cx.warp_wait(L::kCvt + KV, cvt++ & 1)) return;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 lo, hi;
+                        fp8x4_to_bf16<FMT>(raw[c].x, lo.x, lo.y);
+                        fp8x4_to_bf16<FMT>(raw[c].y, lo.z, lo.w);
+                        fp8x4_to_bf16<FMT>(raw[c].z, hi.x, hi.y);
+                        fp8x4_to_bf16<FMT>(raw[c].w, hi.z, hi.w);
+                        char* reg = slot + h * L::kRegion;
+                        *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * c)) = lo;
+                        *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * c + 1)) = hi;
+                    }
+                }
+            } else if (zero) {
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(smem + L::kRing + vs * L::kSlot + (c >> 3) * L::kRegion + ct * 128 +
-                                              ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(slot + (c >> 3) * L::kRegion + ct * 128 + ((c & 7) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async();
-            mbar_arrive(cx.bar(L::kConvB + vs));
+            mbar_arrive(cx.bar(L::kConvB + s));
         }
         if (!more) return;
         cur = ahead;
@@ -462,82 +516,80 @@ struct Row {
     float m, top, l;
 };
 
-// One tile of this thread's row: S at column s of its lane becomes P.  TAIL: only the first
-// `valid` columns are tokens.
-template <int D, bool FP8, bool TAIL>
-__device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
-                                             const float* sv, float c2, Row& r) {
-    float v[32];
-    float mx = kNegInf;
+// Columns from `valid` on are no tokens.
+__device__ __forceinline__ void mask32(float (&v)[32], int valid) {
 #pragma unroll
-    for (int c = 0; c < kTok / 32; ++c) {
-        tmem_ld32(s + 32 * c, v);
+    for (int i = 0; i < 32; ++i)
+        if (i >= valid) v[i] = kNegInf;
+}
+
+// One job: S at column s of this thread's lane becomes P.  O (column o) is idle while it
+// lasts: the product into S came after the last one into O.
+template <int D, bool FP8>
+__device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
+                                            const float* sv, float c2, Row& r) {
+    float v[32];
+    float mx0 = kNegInf, mx1 = kNegInf;
+#pragma unroll 1
+    for (int c = 0; c < kTok; c += 32) {
+        tmem_ld32(s + c, v);
         wait_ld(v);
+        if (c + 32 > valid) mask32(v, valid - c);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (FP8) k = *reinterpret_cast<const float4*>(sk + 32 * c + i);
-            const float kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float x = FP8 ? v[i + u] * kk[u] : v[i + u];
-                if (TAIL && 32 * c + i + u >= valid) x = kNegInf;
-                mx = fmaxf(mx, x);
+            if (FP8) {
+                k = *reinterpret_cast<const float4*>(sk + c + i);
+                v[i] *= k.x; v[i + 1] *= k.y; v[i + 2] *= k.z; v[i + 3] *= k.w;
             }
+            mx0 = fmaxf(fmaxf(mx0, v[i]), v[i + 1]);
+            mx1 = fmaxf(fmaxf(mx1, v[i + 2]), v[i + 3]);
         }
     }
-    if (!FP8) mx *= c2;
-    r.top = first ? mx : fmaxf(r.top, mx);
+    const float mx = FP8 ? fmaxf(mx0, mx1) : fmaxf(mx0, mx1) * c2;
+    r.top = fmaxf(r.top, mx);
     if (first) {
         r.m = mx == kNegInf ? 0.f : mx;
-        r.l = 0.f;
     } else {
         const bool move = mx > r.m + 8.f;
-        if (__any_sync(kFull, move)) {   // O is idle: the product into S came after the last one into O
+        if (__any_sync(kFull, move)) {
             const float f = move ? ex2(r.m - mx) : 1.f;
             r.l *= f;
             if (move) r.m = mx;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(o + 32 * c, v);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                tmem_ld32(o + c, v);
                 wait_ld(v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= f;
-                tmem_st32(o + 32 * c, v);
+                tmem_st32(o + c, v);
             }
         }
     }
     const float m = r.m;
     float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-    for (int c = 0; c < kTok / 32; ++c) {
-        tmem_ld32(s + 32 * c, v);
+#pragma unroll 1
+    for (int c = 0; c < kTok; c += 32) {
+        tmem_ld32(s + c, v);
         wait_ld(v);
+        if (c + 32 > valid) mask32(v, valid - c);
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            float4 k = make_float4(c2, c2, c2, c2), f = make_float4(1.f, 1.f, 1.f, 1.f);
+            float4 k = make_float4(c2, c2, c2, c2);
+            if (FP8) k = *reinterpret_cast<const float4*>(sk + c + i);
+            float p0 = ex2(fmaf(v[i], k.x, -m)), p1 = ex2(fmaf(v[i + 1], k.y, -m));
+            float p2 = ex2(fmaf(v[i + 2], k.z, -m)), p3 = ex2(fmaf(v[i + 3], k.w, -m));
+            l0 += p0 + p2;
+            l1 += p1 + p3;
             if (FP8) {
-                k = *reinterpret_cast<const float4*>(sk + 32 * c + i);
-                f = *reinterpret_cast<const float4*>(sv + 32 * c + i);
+                const float4 f = *reinterpret_cast<const float4*>(sv + c + i);
+                p0 *= f.x; p1 *= f.y; p2 *= f.z; p3 *= f.w;
             }
-            const float kk[4] = {k.x, k.y, k.z, k.w}, ff[4] = {f.x, f.y, f.z, f.w};
-            float p[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                p[u] = ex2(fmaf(v[i + u], kk[u], -m));
-                if (TAIL && 32 * c + i + u >= valid) p[u] = 0.f;
-            }
-            l0 += p[0] + p[2];
-            l1 += p[1] + p[3];
-            if (FP8) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) p[u] *= ff[u];
-            }
-            pk[i / 2] = pack_bf16(p[0], p[1]);
-            pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
+            pk[i / 2] = pack_bf16(p0, p1);
+            pk[i / 2 + 1] = pack_bf16(p2, p3);
         }
-        tmem_st16(s + 16 * c, pk);   // over columns of S that have been read
+        tmem_st16(s + c / 2, pk);   // over columns of S that have been read
     }
     r.l += l0 + l1;
     wait_st();
@@ -550,69 +602,75 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b), o = lane + tmem_o<D>(b);
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * b * kTok;
-    const float* sv = sk + kTok;
-    int j = 0, seg = 0, scales = 0;
+    int seg = 0, f = 0, xch = 0;   // segments, FP8 tiles and exchanges so far
+    uint32_t s_ph = 0;         // parity of this warpgroup's next S
     while (w.segment()) {
-        const int n = w.i_end - w.i, j0 = j;
+        const bool two = w.two();
+        const int n = w.i_end - w.i;
         Row r{0.f, kNegInf, 0.f};
         bool first = true;
-        for (int x = 0; x < n; ++x, ++j) {
+#pragma unroll 1
+        for (int x = 0; x < n; ++x) {
             const Tile t = w.tile();
-            if ((j & 1) != b) continue;
-            if (t.fp8 && !cx.warp_wait(L::kScFull + b, scales++ & 1)) return;
-            if (!cx.warp_wait(L::kSFull + b, (j >> 1) & 1)) return;
+            const int z = f & 1, use = (f >> 1) & 1;
+            f += t.fp8;
+            if (!two && (x & 1) != b) continue;
+            if (!cx.warp_wait(L::kSFull + b, s_ph)) return;
+            s_ph ^= 1u;
             fence_after();
-            if (t.valid == kTok) {
-                if (t.fp8) softmax_tile<D, true, false>(s, o, first, kTok, sk, sv, c2, r);
-                else softmax_tile<D, false, false>(s, o, first, kTok, sk, sv, c2, r);
+            if (t.fp8) {
+                if (!cx.warp_wait(L::kScFull + z, use)) return;   // complete: K came after the scales
+                const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
+                softmax_job<D, true>(s, o, first, t.valid, sk, sk + kTok, c2, r);
             } else {
-                if (t.fp8) softmax_tile<D, true, true>(s, o, first, t.valid, sk, sv, c2, r);
-                else softmax_tile<D, false, true>(s, o, first, t.valid, sk, sv, c2, r);
+                softmax_job<D, false>(s, o, first, t.valid, nullptr, nullptr, c2, r);
             }
             first = false;
             fence_before();
             mbar_arrive(cx.bar(L::kPFull + b));
-            if (t.fp8) mbar_arrive(cx.bar(L::kScFree + b));
+            if (t.fp8) mbar_arrive_n(cx.bar(L::kScFree + z), two ? 1 : 2);   // 256 in all, whoever read them
         }
-        // the segment's partial: both warpgroups' O under one reference, half the columns each
         if (!cx.warp_wait(L::kOFull, seg & 1)) return;
         fence_after();
-        tmem_st4(s, r.m, r.top, r.l, 0.f);   // S and P are idle: the state goes to the other warpgroup through them
-        wait_st();
-        fence_before();
-        mbar_arrive(cx.bar(L::kXch));
-        if (!cx.warp_wait(L::kXch, seg & 1)) return;
-        fence_after();
-        float y[4];
-        tmem_ld4(lane + tmem_s(b ^ 1), y);
-        wait_ld(y);
-        const bool mine = n > 1 || (j0 & 1) == b, theirs = n > 1 || (j0 & 1) != b;   // who had a tile
+        // The segment's partial.  With one tile of rows both warpgroups hold half of the tokens:
+        // each gets the other's state (through S, idle now) and adds half of the columns.
+        float y[4] = {0.f, kNegInf, 0.f, 0.f};
+        if (!two) {
+            tmem_st4(s, r.m, r.top, r.l, 0.f);
+            wait_st();
+            fence_before();
+            mbar_arrive(cx.bar(L::kXch));
+            if (!cx.warp_wait(L::kXch, xch++ & 1)) return;
+            fence_after();
+            tmem_ld4(lane + tmem_s(b ^ 1), y);
+            wait_ld(y);
+        }
+        const bool mine = two || n > b, theirs = !two && n > (b ^ 1);   // who had a tile
         const float top = fmaxf(r.top, y[1]);   // a warpgroup without one has -inf
         // raw units for the join; what the rounding of the maximum moves goes into the weights
         const double c2d = a.p.inv_sqrt_d * 1.4426950408889634;
         const float M = top == kNegInf ? kNegInf : top / c2;
         const double at = top == kNegInf ? 0.0 : (double)M * c2d;
-        const float w_mine = mine ? exp2f((float)((double)r.m - at)) : 0.f;
-        const float w_theirs = theirs ? exp2f((float)((double)y[0] - at)) : 0.f;
+        const float w_mine = exp2f((float)((double)r.m - at)), w_theirs = theirs ? exp2f((float)((double)y[0] - at)) : 0.f;
         const float sum = (mine ? r.l * w_mine : 0.f) + (theirs ? y[2] * w_theirs : 0.f);
-        const int slot = cta + w.unit0 + w.m;
-        const int rows = min(a.per_tile, w.r.nb - w.m * a.per_tile) * d.G;
+        const int slot = cta + w.unit0 + w.m, rt = two ? b : 0;
+        const int rows = min(a.per_tile, w.r.nb - w.first_branch() - rt * a.per_tile) * d.G;
         const bool live = row < rows && slot < a.slots;
-        if (live && b == 0) a.part_ml[(size_t)slot * kRows + row] = make_float2(M, sum);
-        float* out = a.part_o + ((size_t)slot * kRows + row) * D + b * (D / 2);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
+        const size_t at_slot = (size_t)slot * a.row_tiles + rt;
+        if (live && (two || b == 0)) a.part_ml[at_slot * kRows + row] = make_float2(M, sum);
+        float4* out = a.part_o + at_slot * (D / 4) * kRows + row;
+        const int c_begin = two ? 0 : b * (D / 2), c_end = two ? D : c_begin + D / 2;
+#pragma unroll 1
+        for (int c = c_begin; c < c_end; c += 32) {
             float u[32], v[32];
-            const uint32_t col = b * (D / 2) + 32 * c;
             if (mine) {
-                tmem_ld32(o + col, u);
+                tmem_ld32(o + c, u);
                 wait_ld(u);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = mine ? u[i] * w_mine : 0.f;
             if (theirs) {
-                tmem_ld32(lane + tmem_o<D>(b ^ 1) + col, v);
+                tmem_ld32(lane + tmem_o<D>(b ^ 1) + c, v);
                 wait_ld(v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) u[i] = fmaf(v[i], w_theirs, u[i]);
@@ -620,7 +678,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             if (live) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4*>(out + 32 * c + i) = make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                    __stcg(out + (size_t)((c + i) / 4) * kRows, make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]));
             }
         }
         fence_before();
@@ -629,82 +687,83 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     }
 }
 
-// Tiles and units before every row, for the join (one warp).
-__device__ void write_starts(const AttnArgs& a) {
-    const int lane = threadIdx.x & 31;
-    long long t = 0, u = 0;
-    for (int r0 = 0; r0 < a.p.d.R; r0 += 32) {
-        long long x = 0, y = 0;
-        if (r0 + lane < a.p.d.R) {
-            const RowInfo r = row_info(a, r0 + lane);
-            x = (long long)r.mt * (r.T16 + r.T8);
-            y = r.mt;
-        }
-        long long sx = x, sy = y;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const long long px = __shfl_up_sync(kFull, sx, m), py = __shfl_up_sync(kFull, sy, m);
-            if (lane >= m) {
-                sx += px;
-                sy += py;
-            }
-        }
-        if (r0 + lane < a.p.d.R) a.starts[r0 + lane] = make_longlong2(t + sx - x, u + sy - y);
-        t += __shfl_sync(kFull, sx, 31);
-        u += __shfl_sync(kFull, sy, 31);
-    }
-    if (lane == 0) a.starts[a.p.d.R] = make_longlong2(t, u);
-}
-
-// This CTA's run: a block scan of the rows' tiles (threads own contiguous rows), then the
-// thread whose rows hold the run's first tile hands over where that is.
-template <int D>
-__device__ __forceinline__ Sched schedule(const AttnArgs& a, char* smem) {
-    using L = Smem<D>;
-    Sched* out = reinterpret_cast<Sched*>(smem + L::kSched);
-    longlong2* sums = reinterpret_cast<longlong2*>(smem + L::kSums);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.p.d.R;
-    const int per = (R + kThreads - 1) / kThreads, r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    long long x = 0, y = 0;
-    for (int r = r0; r < r1; ++r) {
-        const RowInfo i = row_info(a, r);
-        x += (long long)i.mt * (i.T16 + i.T8);
-        y += i.mt;
-    }
-    long long sx = x, sy = y;
+// Inclusive scan of (x, y) over a warp.
+__device__ __forceinline__ int2 warp_scan(int2 v) {
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const long long px = __shfl_up_sync(kFull, sx, m), py = __shfl_up_sync(kFull, sy, m);
-        if (lane >= m) {
-            sx += px;
-            sy += py;
+        const int px = __shfl_up_sync(kFull, v.x, m), py = __shfl_up_sync(kFull, v.y, m);
+        if ((threadIdx.x & 31) >= m) {
+            v.x += px;
+            v.y += py;
         }
     }
-    if (lane == 31) sums[warp] = make_longlong2(sx, sy);
-    if (tid == 0) *out = Sched{0, 0, 0, 0, 0};
+    return v;
+}
+
+// List places and units before every row, for the join (one warp).
+__device__ void write_starts(const AttnArgs& a) {
+    const int lane = threadIdx.x & 31, R = a.p.d.R;
+    int t = 0, u = 0;
+    for (int r0 = 0; r0 < R; r0 += 32) {
+        int2 x = make_int2(0, 0);
+        if (r0 + lane < R) {
+            const RowInfo r = row_info(a, r0 + lane);
+            x = make_int2(r.mt * unit_len(r), r.mt);
+        }
+        const int2 s = warp_scan(x);
+        if (r0 + lane < R) a.starts[r0 + lane] = make_int2(t + s.x - x.x, u + s.y - x.y);
+        t += __shfl_sync(kFull, s.x, 31);
+        u += __shfl_sync(kFull, s.y, 31);
+    }
+    if (lane == 0) a.starts[R] = make_int2(t, u);
+}
+
+// This CTA's run: a block scan over the rows (threads own contiguous ones), then the thread
+// whose rows hold the run's first place hands over where that is.
+template <int D>
+__device__ __forceinline__ void schedule(const AttnArgs& a, char* smem) {
+    using L = Smem<D>;
+    Sched* out = reinterpret_cast<Sched*>(smem + L::kSched);
+    int2* sums = reinterpret_cast<int2*>(smem + L::kSums);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.p.d.R;
+    const int per = (R + kThreads - 1) / kThreads, r0 = min(R, tid * per), r1 = min(R, r0 + per);
+    RowInfo first{};
+    int2 x = make_int2(0, 0);
+    for (int r = r0; r < r1; ++r) {
+        const RowInfo i = row_info(a, r);
+        if (r == r0) first = i;
+        x.x += i.mt * unit_len(i);
+        x.y += i.mt;
+    }
+    const int2 s = warp_scan(x);
+    if (lane == 31) sums[warp] = s;
+    if (tid == 0) out->v = out->v_end = 0;
     __syncthreads();
-    long long T = 0, tx = sx - x, ty = sy - y;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        const longlong2 z = sums[i];
-        T += z.x;
+    int V = 0, at = s.x - x.x, units = s.y - x.y;
+    for (int i = 0; i < kWarps; ++i) {
+        const int2 z = sums[i];
+        V += z.x;
         if (i < warp) {
-            tx += z.x;
-            ty += z.y;
+            at += z.x;
+            units += z.y;
         }
     }
-    const int P = (int)min((long long)gridDim.x, T);
-    if ((int)blockIdx.x < P) {
-        const long long t0 = run_begin(T, P, blockIdx.x), t1 = run_begin(T, P, blockIdx.x + 1);
-        for (int r = r0; r < r1; ++r) {
-            const RowInfo i = row_info(a, r);
-            const long long n = (long long)i.mt * (i.T16 + i.T8);
-            if (t0 >= tx && t0 < tx + n) *out = Sched{t0, t1, tx, r, (int)ty};
-            tx += n;
-            ty += i.mt;
+    if (V > 0 && r0 < r1) {
+        const Runs runs(V, gridDim.x);
+        if ((int)blockIdx.x < runs.P) {
+            const int v0 = runs.begin(blockIdx.x);
+            if (v0 >= at && v0 < at + x.x) {
+                for (int r = r0; r < r1; ++r) {
+                    const RowInfo i = r == r0 ? first : row_info(a, r);
+                    const int n = i.mt * unit_len(i);
+                    if (v0 >= at && v0 < at + n) *out = Sched{v0, runs.begin(blockIdx.x + 1), at, r, units, i};
+                    at += n;
+                    units += i.mt;
+                }
+            }
         }
     }
     __syncthreads();
-    return *out;
 }
 
 template <int D, int FMT>
@@ -713,56 +772,59 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
-    if (tid == 0) {
-        prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
-        prefetch_map(&a.tm_v8);
-    }
-    if (!a.p.early_start) pdl_wait();
     const uint32_t base = smem_u32(smem);
     if (base & 1023) {   // the swizzled tiles need it; the CTA's shared memory starts there
-        if (tid == 0) atomicOr(a.p.c.status, ARKV_STATUS_TIMEOUT);
         pdl_wait();
+        if (tid == 0) atomicOr(a.p.c.status, ARKV_STATUS_TIMEOUT);
         return;
     }
     int* misc = reinterpret_cast<int*>(smem + L::kMisc);
     Ctx cx{base + L::kBars, misc + 1, a.p.c.status};
-    if (tid == 0) {
-        for (int i = 0; i < L::kNumBars; ++i) {
-            int n = 1;
-            if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || i == L::kPFull || i == L::kPFull + 1 || i == L::kScFull ||
-                i == L::kScFull + 1 || i == L::kScFree || i == L::kScFree + 1 || i == L::kCvt)
-                n = 128;
-            if (i == L::kXch || i == L::kEpi) n = 256;
-            mbar_init(cx.bar(i), n);
-        }
-        misc[1] = 0;
+    // what needs nothing of the previous kernel comes before the wait for it
+    if (warp == 2) tmem_alloc(base + L::kMisc, kTmemCols);
+    if (tid < L::kNumBars) {
+        const int i = tid;
+        int n = 1;
+        if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 2) ||
+            (i >= L::kScFull && i < L::kScFull + 2) || i >= L::kCvt)
+            n = 128;
+        if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + 2)) n = 256;
+        mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
-    const Sched sched = schedule<D>(a, smem);
-    const bool busy = sched.t < sched.t_end;   // the same for the whole CTA
-    if (busy && warp == 2) tmem_alloc(base + L::kMisc, kTmemCols);
-    __syncthreads();
+    if (warp == 3 && lane == 0) {
+        misc[1] = 0;
+        prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
+        prefetch_map(&a.tm_v8);
+    }
+    if (!a.p.early_start) pdl_wait();
+    schedule<D>(a, smem);
+    const Sched sched = *reinterpret_cast<const Sched*>(smem + L::kSched);
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+    if (sched.v < sched.v_end) {   // the same for the whole CTA
+        if (warp == 0) {
+            if (lane == 0) produce<D>(a, cx, base, Walk(a, sched));
+        } else if (warp == 1) {
+            if (lane == 0) {
+                pdl_wait();   // bounded waits start when the previous kernel has finished
+                multiply<D>(a, cx, base, tmem, Walk(a, sched));
+            }
+        } else if (warp >= 16) {
+            pdl_wait();
+            convert<D, FMT, 1>(a, cx, smem, tid - 512, Walk(a, sched));
+        } else if (warp >= 12) {
+            pdl_wait();
+            convert<D, FMT, 0>(a, cx, smem, tid - 384, Walk(a, sched));
+        } else if (warp >= 4) {
+            pdl_wait();
+            softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2, Walk(a, sched), blockIdx.x);
+        }
+    }
     if (blockIdx.x == 0 && warp == 3) {   // the workspace is the previous call's until it has finished
         pdl_wait();
         write_starts(a);
-    }
-    if (!busy) return;
-    fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
-    if (warp == 0) {
-        if (lane == 0) produce<D>(a, cx, base, Walk(a, sched));
-    } else if (warp == 1) {
-        if (lane == 0) {
-            pdl_wait();   // bounded waits start when the previous kernel has finished
-            multiply<D>(a, cx, base, tmem, Walk(a, sched));
-        }
-    } else if (warp >= 12) {
-        pdl_wait();
-        convert<D, FMT>(a, cx, smem, tid - 384, Walk(a, sched));
-    } else if (warp >= 4) {
-        pdl_wait();
-        softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2, Walk(a, sched), blockIdx.x);
     }
     __syncwarp();
     fence_before();
@@ -774,107 +836,94 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ join
-// One warp per (branch, query head): the partials of its row in CTA order and the own part,
-// (M, L, o) joined in float32, o rounded to bf16.  The partials' loads of a batch are all in
-// flight at once.
+// One block per (branch, key head): thread = (4 dimensions, query of the group).  The partials
+// of the row in CTA order and the own part, joined in float32; o is rounded to bf16.  The
+// loads of a batch of partials are all in flight at once.
 template <int D>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
-    constexpr int VEC = D / 32, kBatch = 8;
+__global__ void __launch_bounds__(D) prefix_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
+    constexpr int kBatch = 12;
     const LayerDims& d = a.p.d;
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int jq = threadIdx.x & 3, c4 = threadIdx.x >> 2;
+    const int b = blockIdx.x / d.hkv, g = blockIdx.x - b * d.hkv;
     pdl_launch_dependents();
     pdl_wait();
-    if (item >= (long long)a.p.branches * d.hq) return;
-    const int b = (int)(item / d.hq), h = (int)(item % d.hq), g = h / d.G, jq = h % d.G;
+    if (jq >= d.G) return;
+    const size_t mi = (size_t)blockIdx.x * 4 + jq, at = (((size_t)b * d.hq + g * d.G + jq) * D) / 4 + c4;
+    float2 own = make_float2(kNegInf, 0.f);
+    float4 o_own = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.p.ml_own) {
+        own = a.p.ml_own[mi];
+        o_own = reinterpret_cast<const float4*>(a.p.o_own)[at];
+    }
     int pre = 0, b0 = 0;
     bool has = true;
     if (a.p.branch_start) {   // the last prefix that starts at or before b
-        int lo = 0, hi = d.batch;   // starts[lo] <= b < starts[hi], sentinels at both ends
+        int lo = 0, hi = d.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (a.p.branch_start[mid] <= b) lo = mid;
+            if (__ldg(a.p.branch_start + mid) <= b) lo = mid;
             else hi = mid;
         }
         pre = lo;
-        const int s = a.p.branch_start[pre];
-        has = s <= b && b < a.p.branch_start[pre + 1];
+        const int s = __ldg(a.p.branch_start + pre);
+        has = s <= b && b < __ldg(a.p.branch_start + pre + 1);
         b0 = max(s, 0);
     }
-    const size_t mi = ((size_t)b * d.hkv + g) * 4 + jq;
-    const size_t at = (size_t)item * D + VEC * lane;
-    float M = kNegInf, L = 0.f, acc[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-    if (a.p.ml_own) {
-        const float2 own = a.p.ml_own[mi];
-        if (own.y != 0.f) {
-            M = own.x;
-            L = own.y;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] = own.y * a.p.o_own[at + e];
-        }
+    float M = kNegInf, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (own.y != 0.f) {   // L = 0: no own tokens
+        M = own.x;
+        L = own.y;
+        acc = make_float4(L * o_own.x, L * o_own.y, L * o_own.z, L * o_own.w);
     }
     if (has) {
         const int row = pre * d.hkv + g;
-        const long long T = a.starts[d.R].x;
-        const longlong2 st = a.starts[row];
+        const Runs runs(a.starts[d.R].x, ctas);
+        const int2 st = a.starts[row];
         const RowInfo r = row_info(a, row);
-        const int m = (b - b0) / a.per_tile, tiles = r.T16 + r.T8;
-        if (tiles > 0) {
-            const long long t0 = st.x + (long long)m * tiles;
-            const int P = (int)min((long long)ctas, T), c0 = run_of(T, P, t0), c1 = run_of(T, P, t0 + tiles - 1);
-            const int unit = (int)st.y + m, rr = (b - b0 - m * a.per_tile) * d.G + jq;
+        const int len = unit_len(r);
+        if (len > 0) {
+            const int per_unit = a.row_tiles * a.per_tile, m = (b - b0) / per_unit, in_unit = b - b0 - m * per_unit;
+            const int rt = in_unit / a.per_tile, rr = (in_unit - rt * a.per_tile) * d.G + jq;
+            const int v = st.x + m * len, c0 = runs.of(v + kSegCost), c1 = runs.of(v + len - 1), unit = st.y + m;
+            auto slot = [&](int c) { return (size_t)min(c + unit, a.slots - 1) * a.row_tiles + rt; };
             for (int c = c0; c <= c1; c += kBatch) {
-                const int cnt = min(kBatch, c1 - c + 1);
-                auto slot = [&](int q) { return min(c + q + unit, a.slots - 1); };
-                float2 ml = make_float2(kNegInf, 0.f);
-                if (lane < cnt) ml = __ldcg(a.part_ml + (size_t)slot(lane) * kRows + rr);
-                float v[kBatch][VEC];
+                float2 ml[kBatch];
+                float4 x[kBatch];
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
-                    const float* src = a.part_o + ((size_t)slot(q) * kRows + rr) * D + VEC * lane;
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 2) {
-                        const float2 x = q < cnt ? __ldcg(reinterpret_cast<const float2*>(src + e)) : make_float2(0.f, 0.f);
-                        v[q][e] = x.x;
-                        v[q][e + 1] = x.y;
+                    ml[q] = make_float2(kNegInf, 0.f);
+                    x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + q <= c1) {
+                        const size_t s = slot(c + q);
+                        ml[q] = __ldcg(a.part_ml + s * kRows + rr);
+                        x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + rr);
                     }
                 }
-                float mb = ml.y != 0.f ? ml.x : kNegInf;
+                float mb = M;
 #pragma unroll
-                for (int k = 16; k >= 1; k >>= 1) mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, k));
+                for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, ml[q].y != 0.f ? ml[q].x : kNegInf);
                 if (mb > M) {
                     const float f = M == kNegInf ? 0.f : exp_scaled(M, mb, a.p.inv_sqrt_d);
                     L *= f;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[e] *= f;
+                    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
                     M = mb;
                 }
-                // a partial without weight has l = 0; a NaN sum goes through
-                const float wl = ml.y == 0.f ? 0.f : (ml.x == M ? 1.f : exp_scaled(ml.x, M, a.p.inv_sqrt_d));
-                float part = ml.y * wl;
-#pragma unroll
-                for (int k = 16; k >= 1; k >>= 1) part += __shfl_xor_sync(kFull, part, k);
-                L += part;
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
-                    const float f = __shfl_sync(kFull, wl, q);
-                    if (q < cnt && f != 0.f) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(v[q][e], f, acc[e]);
-                    }
+                    if (ml[q].y == 0.f) continue;   // a partial without weight; a NaN goes through
+                    const float f = ml[q].x == M ? 1.f : exp_scaled(ml[q].x, M, a.p.inv_sqrt_d);
+                    L = fmaf(ml[q].y, f, L);
+                    acc.x = fmaf(x[q].x, f, acc.x); acc.y = fmaf(x[q].y, f, acc.y);
+                    acc.z = fmaf(x[q].z, f, acc.z); acc.w = fmaf(x[q].w, f, acc.w);
                 }
             }
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint32_t out[VEC / 2];
-#pragma unroll
-    for (int e = 0; e < VEC; e += 2) out[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-    if constexpr (VEC == 4) *reinterpret_cast<uint2*>(a.p.o + at) = make_uint2(out[0], out[1]);
-    else *reinterpret_cast<uint32_t*>(a.p.o + at) = out[0];
-    if (lane == 0 && a.p.ml) a.p.ml[mi] = make_float2(M, L);
+    reinterpret_cast<uint2*>(a.p.o)[at] =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (c4 == 0 && a.p.ml) a.p.ml[mi] = make_float2(M, L);
 }
 
 // ------------------------------------------------------------------ host
@@ -919,21 +968,26 @@ bool make_q_map(CUtensorMap* m, const void* base, const LayerDims& d, int branch
 
 struct PrefixWs {
     size_t part_o, part_ml, starts, total;
-    int slots, per_tile;
+    long long slots, units, places;
+    int per_tile, row_tiles;
 };
 
-// A segment's partial goes to slot (CTA + unit): along the list of tiles each next segment
-// raises one of the two, so the slots differ, and there are at most CTAs + units of them.
+// A segment's partial goes to slot (CTA + unit): along the list each next segment raises one
+// of the two, so the slots differ, and there are at most CTAs + units of them.  places: the
+// longest the list can get.
 PrefixWs ws_layout(const LayerDims& d, int branches) {
     PrefixWs w{};
     w.per_tile = kRows / d.G;
-    const long long units = (long long)d.hkv * (d.batch + branches / w.per_tile);
-    w.slots = (int)(kMaxCtas + units);
+    w.row_tiles = branches > w.per_tile ? 2 : 1;
+    w.units = (long long)d.hkv * (d.batch + branches / (w.row_tiles * w.per_tile));
+    w.places = w.units * (((long long)d.cap_o + kTok - 1) / kTok + ((long long)d.cap_q + kTok - 1) / kTok + kSegCost);
+    w.slots = kMaxCtas + w.units;
     auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t rows = (size_t)w.slots * w.row_tiles * kRows;
     size_t off = 0;
-    w.starts = off;  off = al(off + sizeof(longlong2) * ((size_t)d.R + 1));
-    w.part_ml = off; off = al(off + sizeof(float2) * kRows * (size_t)w.slots);
-    w.part_o = off;  off = al(off + sizeof(float) * kRows * (size_t)d.D * w.slots);
+    w.starts = off;  off = al(off + sizeof(int2) * ((size_t)d.R + 1));
+    w.part_ml = off; off = al(off + sizeof(float2) * rows);
+    w.part_o = off;  off = al(off + sizeof(float) * rows * d.D);
     w.total = off;
     return w;
 }
@@ -945,13 +999,16 @@ size_t prefix_ws_bytes(const LayerDims& d, int branches) { return ws_layout(d, b
 cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) {
     const LayerDims& d = p.d;
     const PrefixWs w = ws_layout(d, p.branches);
+    const long long blocks = (long long)p.branches * d.hkv;
+    if (w.places > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidValue;
     AttnArgs a{};
     a.p = p;
-    a.slots = w.slots;
+    a.slots = (int)w.slots;
     a.per_tile = w.per_tile;
-    a.starts = reinterpret_cast<longlong2*>((char*)ws + w.starts);
+    a.row_tiles = w.row_tiles;
+    a.starts = reinterpret_cast<int2*>((char*)ws + w.starts);
     a.part_ml = reinterpret_cast<float2*>((char*)ws + w.part_ml);
-    a.part_o = reinterpret_cast<float*>((char*)ws + w.part_o);
+    a.part_o = reinterpret_cast<float4*>((char*)ws + w.part_o);
     const long long r16 = (long long)d.R * d.cap_o, r8 = (long long)d.R * d.cap_q;
     if (!make_q_map(&a.tm_q, p.q, d, p.branches, w.per_tile) || !make_map(&a.tm_k16, p.c.k16, false, d.D, r16) ||
         !make_map(&a.tm_v16, p.c.v16, false, d.D, r16) || !make_map(&a.tm_k8, p.c.k8, true, d.D, r8) ||
@@ -961,10 +1018,8 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    // one CTA an SM, at most one a tile of the fullest prefixes
-    const long long most = (w.slots - kMaxCtas) * (((long long)d.cap_o + kTok - 1) / kTok + (d.cap_q + kTok - 1) / kTok);
-    long long ctas = sms < kMaxCtas ? sms : kMaxCtas;
-    if (ctas > most) ctas = most;
+    long long ctas = sms < kMaxCtas ? sms : kMaxCtas;   // one an SM
+    if (ctas > w.places) ctas = w.places;
     static unsigned char done[4][64];
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -980,8 +1035,8 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
         lc.blockDim = dim3(kThreads);
         lc.dynamicSmemBytes = (size_t)bytes;
         if ((err = cudaLaunchKernelEx(&lc, kernel, a)) != cudaSuccess) return err;
-        lc.gridDim = dim3((unsigned)(((long long)p.branches * d.hq + 3) / 4));
-        lc.blockDim = dim3(128);
+        lc.gridDim = dim3((unsigned)blocks);
+        lc.blockDim = dim3((unsigned)d.D);
         lc.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&lc, join, a, (int)ctas);
     };
