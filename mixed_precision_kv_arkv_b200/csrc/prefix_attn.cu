@@ -106,16 +106,21 @@ struct AttnArgs {
     PrefixParams p;
     float4* part_o;      // [slots][row_tiles][D / 4][128 rows]: a warp's rows side by side
     float2* part_ml;     // [slots][row_tiles][128]
-    int2* starts;        // [R + 1]: list places and units before each row
+    int2* unit_slots;    // [R][row_units]: the first and last slot with a partial of a unit
+    int row_units;       // units of a row, at most
+    unsigned div_hkv, div_unit, div_ctas;   // divisors hkv, branches of a unit, CTAs (see divided)
     int slots;
     int per_tile;        // branches of one tile of rows
     int row_tiles;       // tiles of rows of a unit, at most
 };
 
+// x / d for x d < 2^32, with m = floor(2^32 / d) + 1 made by the host (d = 1: m = 0).
+__device__ __forceinline__ int divided(int x, unsigned m) { return m ? (int)__umulhi((unsigned)x, m) : x; }
+
 __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int row) {
     const LayerDims& d = a.p.d;
     RowInfo r;
-    const int pre = row / d.hkv;
+    const int pre = divided(row, a.div_hkv);
     r.n16 = __ldg(a.p.c.n_bf16 + row);
     r.n8 = __ldg(a.p.c.n_fp8 + row);
     int b0 = 0, b1 = a.p.branches;
@@ -126,7 +131,7 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int row) {
     }
     r.b0 = b0;
     r.nb = b1 - b0;
-    r.mt = (r.nb + a.row_tiles * a.per_tile - 1) / (a.row_tiles * a.per_tile);
+    r.mt = divided(r.nb + a.row_tiles * a.per_tile - 1, a.div_unit);
     r.n16 = min(max(r.n16, 0), d.cap_o);   // clamped to the capacities
     r.n8 = min(max(r.n8, 0), d.cap_q);
     r.T16 = (r.n16 + kTok - 1) / kTok;
@@ -136,20 +141,22 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int row) {
 // Places a unit of this row takes in the list.
 __device__ __forceinline__ int unit_len(const RowInfo& r) { return r.T16 + r.T8 > 0 ? r.T16 + r.T8 + kSegCost : 0; }
 
-// Run c of P over V places begins at c V / P (V = q P + r, so the product stays small).
+// Run c of P CTAs over V places begins at c V / P (V = q P + r, so the product stays small).
 struct Runs {
-    int V, P, q, r;
-    __device__ __forceinline__ Runs(int total, int ctas) : V(total), P(min(ctas, total)) {
-        q = P > 0 ? V / P : 0;
-        r = V - q * P;
+    int P, q, r;
+    unsigned m;
+    __device__ __forceinline__ Runs(int V, int ctas, unsigned div_ctas) : P(ctas), m(div_ctas) {
+        if (V < ctas) {   // a place each
+            P = V;
+            q = 1;
+            r = 0;
+        } else {
+            q = divided(V, m);   // one too many at most: V may be past 2^32 / ctas
+            if (q * P > V) --q;
+            r = V - q * P;
+        }
     }
-    __device__ __forceinline__ int begin(int c) const { return c * q + c * r / P; }
-    __device__ __forceinline__ int of(int v) const {   // the run that holds place v
-        int c = min((int)((float)v / (float)V * (float)P), P - 1);
-        while (c > 0 && begin(c) > v) --c;
-        while (begin(c + 1) <= v) ++c;
-        return c;
-    }
+    __device__ __forceinline__ int begin(int c) const { return c * q + divided(c * r, m); }
 };
 
 struct Tile {
@@ -167,7 +174,7 @@ struct Walk {
     __device__ __forceinline__ Walk(const AttnArgs& args, const Sched& s)
         : a(args), v(s.v), v_end(s.v_end), base(s.base), row(s.row), m(0), unit0(s.units), r(s.r), T(r.T16 + r.T8), i(0),
           i_end(0), err(0), f8(0) {
-        if (T > 0) {
+        if (r.mt > 1) {
             m = (v - base) / (T + kSegCost);
             base += m * (T + kSegCost);
         }
@@ -516,82 +523,95 @@ struct Row {
     float m, top, l;
 };
 
-// Columns from `valid` on are no tokens.
-__device__ __forceinline__ void mask32(float (&v)[32], int valid) {
+// Sixteen columns of S: those from `valid` on are no tokens; times their K scales (FP8).
+template <bool FP8>
+__device__ __forceinline__ void logits16(float (&v)[16], int valid, const float* sk) {
+    float4 k[4];
+    if (FP8) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i >= valid) v[i] = kNegInf;
+        for (int i = 0; i < 4; ++i) k[i] = reinterpret_cast<const float4*>(sk)[i];
+    }
+    wait_ld(v);
+    if (valid < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i >= valid) v[i] = kNegInf;
+    }
+    if (FP8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = mul2(make_float2(v[4 * i], v[4 * i + 1]), make_float2(k[i].x, k[i].y));
+            const float2 y = mul2(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(k[i].z, k[i].w));
+            v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = y.x; v[4 * i + 3] = y.y;
+        }
+    }
 }
 
 // One job: S at column s of this thread's lane becomes P.  O (column o) is idle while it
-// lasts: the product into S came after the last one into O.
+// lasts: the product into S came after the last one into O.  S is read twice, 16 columns at
+// a time.
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
                                             const float* sv, float c2, Row& r) {
-    float v[32];
-    float mx0 = kNegInf, mx1 = kNegInf;
+    float v[16];
+    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll 1
-    for (int c = 0; c < kTok; c += 32) {
-        tmem_ld32(s + c, v);
-        wait_ld(v);
-        if (c + 32 > valid) mask32(v, valid - c);
+    for (int c = 0; c < kTok; c += 16) {
+        tmem_ld16(s + c, v);
+        logits16<FP8>(v, valid - c, sk + c);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (FP8) {
-                k = *reinterpret_cast<const float4*>(sk + c + i);
-                v[i] *= k.x; v[i + 1] *= k.y; v[i + 2] *= k.z; v[i + 3] *= k.w;
-            }
-            mx0 = fmaxf(fmaxf(mx0, v[i]), v[i + 1]);
-            mx1 = fmaxf(fmaxf(mx1, v[i + 2]), v[i + 3]);
-        }
+        for (int i = 0; i < 16; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[i + e]), v[i + 4 + e]);
     }
-    const float mx = FP8 ? fmaxf(mx0, mx1) : fmaxf(mx0, mx1) * c2;
-    r.top = fmaxf(r.top, mx);
+    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if (!FP8) top *= c2;
+    r.top = fmaxf(r.top, top);
     if (first) {
-        r.m = mx == kNegInf ? 0.f : mx;
+        r.m = top == kNegInf ? 0.f : top;
     } else {
-        const bool move = mx > r.m + 8.f;
+        const bool move = top > r.m + 8.f;
         if (__any_sync(kFull, move)) {
-            const float f = move ? ex2(r.m - mx) : 1.f;
+            const float f = move ? ex2(r.m - top) : 1.f;
             r.l *= f;
-            if (move) r.m = mx;
+            if (move) r.m = top;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-                tmem_ld32(o + c, v);
-                wait_ld(v);
+                float x[32];
+                tmem_ld32(o + c, x);
+                wait_ld(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= f;
-                tmem_st32(o + c, v);
+                for (int i = 0; i < 32; ++i) x[i] *= f;
+                tmem_st32(o + c, x);
             }
         }
     }
-    const float m = r.m;
-    float l0 = 0.f, l1 = 0.f;
+    const float2 m2 = make_float2(-r.m, -r.m), cc = FP8 ? make_float2(1.f, 1.f) : make_float2(c2, c2);
+    float2 l = make_float2(0.f, 0.f);
 #pragma unroll 1
-    for (int c = 0; c < kTok; c += 32) {
-        tmem_ld32(s + c, v);
-        wait_ld(v);
-        if (c + 32 > valid) mask32(v, valid - c);
-        uint32_t pk[16];
+    for (int c = 0; c < kTok; c += 16) {
+        tmem_ld16(s + c, v);
+        logits16<FP8>(v, valid - c, sk + c);
+        uint32_t pk[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float4 k = make_float4(c2, c2, c2, c2);
-            if (FP8) k = *reinterpret_cast<const float4*>(sk + c + i);
-            float p0 = ex2(fmaf(v[i], k.x, -m)), p1 = ex2(fmaf(v[i + 1], k.y, -m));
-            float p2 = ex2(fmaf(v[i + 2], k.z, -m)), p3 = ex2(fmaf(v[i + 3], k.w, -m));
-            l0 += p0 + p2;
-            l1 += p1 + p3;
+        for (int i = 0; i < 16; i += 4) {
+            float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (FP8) f = *reinterpret_cast<const float4*>(sv + c + i);
+            float2 a = FP8 ? add2(make_float2(v[i], v[i + 1]), m2) : fma2(make_float2(v[i], v[i + 1]), cc, m2);
+            float2 b = FP8 ? add2(make_float2(v[i + 2], v[i + 3]), m2) : fma2(make_float2(v[i + 2], v[i + 3]), cc, m2);
+            a = make_float2(ex2(a.x), ex2(a.y));
+            b = make_float2(ex2(b.x), ex2(b.y));
+            l = add2(l, add2(a, b));
             if (FP8) {
-                const float4 f = *reinterpret_cast<const float4*>(sv + c + i);
-                p0 *= f.x; p1 *= f.y; p2 *= f.z; p3 *= f.w;
+                a = mul2(a, make_float2(f.x, f.y));
+                b = mul2(b, make_float2(f.z, f.w));
             }
-            pk[i / 2] = pack_bf16(p0, p1);
-            pk[i / 2 + 1] = pack_bf16(p2, p3);
+            pk[i / 2] = pack_bf16(a.x, a.y);
+            pk[i / 2 + 1] = pack_bf16(b.x, b.y);
         }
-        tmem_st16(s + c / 2, pk);   // over columns of S that have been read
+        tmem_st8(s + c / 2, pk);   // over columns of S that have been read
     }
-    r.l += l0 + l1;
+    r.l += l.x + l.y;
     wait_st();
 }
 
@@ -606,7 +626,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     uint32_t s_ph = 0;         // parity of this warpgroup's next S
     while (w.segment()) {
         const bool two = w.two();
-        const int n = w.i_end - w.i;
+        const int i0 = w.i, n = w.i_end - i0;
         Row r{0.f, kNegInf, 0.f};
         bool first = true;
 #pragma unroll 1
@@ -648,14 +668,18 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
         const bool mine = two || n > b, theirs = !two && n > (b ^ 1);   // who had a tile
         const float top = fmaxf(r.top, y[1]);   // a warpgroup without one has -inf
         // raw units for the join; what the rounding of the maximum moves goes into the weights
-        const double c2d = a.p.inv_sqrt_d * 1.4426950408889634;
-        const float M = top == kNegInf ? kNegInf : top / c2;
-        const double at = top == kNegInf ? 0.0 : (double)M * c2d;
-        const float w_mine = exp2f((float)((double)r.m - at)), w_theirs = theirs ? exp2f((float)((double)y[0] - at)) : 0.f;
+        const float M = top == kNegInf ? kNegInf : top / c2, at = top == kNegInf ? 0.f : M * c2;
+        const float lo = top == kNegInf ? 0.f : fmaf(M, c2, -at);
+        const float w_mine = ex2(r.m - at - lo), w_theirs = theirs ? ex2(y[0] - at - lo) : 0.f;
         const float sum = (mine ? r.l * w_mine : 0.f) + (theirs ? y[2] * w_theirs : 0.f);
         const int slot = cta + w.unit0 + w.m, rt = two ? b : 0;
         const int rows = min(a.per_tile, w.r.nb - w.first_branch() - rt * a.per_tile) * d.G;
         const bool live = row < rows && slot < a.slots;
+        if (b == 0 && row == 0) {   // the unit's slots, from its first and its last segment
+            int2* us = a.unit_slots + (size_t)w.row * a.row_units + w.m;
+            if (i0 == 0) us->x = slot;
+            if (w.i_end == w.T) us->y = slot;
+        }
         const size_t at_slot = (size_t)slot * a.row_tiles + rt;
         if (live && (two || b == 0)) a.part_ml[at_slot * kRows + row] = make_float2(M, sum);
         float4* out = a.part_o + at_slot * (D / 4) * kRows + row;
@@ -700,44 +724,51 @@ __device__ __forceinline__ int2 warp_scan(int2 v) {
     return v;
 }
 
-// List places and units before every row, for the join (one warp).
-__device__ void write_starts(const AttnArgs& a) {
-    const int lane = threadIdx.x & 31, R = a.p.d.R;
-    int t = 0, u = 0;
-    for (int r0 = 0; r0 < R; r0 += 32) {
-        int2 x = make_int2(0, 0);
-        if (r0 + lane < R) {
-            const RowInfo r = row_info(a, r0 + lane);
-            x = make_int2(r.mt * unit_len(r), r.mt);
-        }
-        const int2 s = warp_scan(x);
-        if (r0 + lane < R) a.starts[r0 + lane] = make_int2(t + s.x - x.x, u + s.y - x.y);
-        t += __shfl_sync(kFull, s.x, 31);
-        u += __shfl_sync(kFull, s.y, 31);
-    }
-    if (lane == 0) a.starts[R] = make_int2(t, u);
+// This CTA's run, up to 32 rows: every warp for itself, a lane a row.
+__device__ __forceinline__ Sched schedule_warp(const AttnArgs& a) {
+    const int lane = threadIdx.x & 31;
+    RowInfo i{};
+    if (lane < a.p.d.R) i = row_info(a, lane);
+    const int n = i.mt * unit_len(i);
+    const int2 s = warp_scan(make_int2(n, i.mt));
+    const int V = __shfl_sync(kFull, s.x, 31), at = s.x - n;
+    Sched out{};
+    const Runs runs(V, gridDim.x, a.div_ctas);
+    if ((int)blockIdx.x >= runs.P) return out;
+    out.v = runs.begin(blockIdx.x);
+    out.v_end = runs.begin(blockIdx.x + 1);
+    const int src = __ffs(__ballot_sync(kFull, out.v >= at && out.v < at + n)) - 1;
+    out.row = src;
+    out.base = __shfl_sync(kFull, at, src);
+    out.units = __shfl_sync(kFull, s.y - i.mt, src);
+    out.r.n16 = __shfl_sync(kFull, i.n16, src);
+    out.r.n8 = __shfl_sync(kFull, i.n8, src);
+    out.r.T16 = (out.r.n16 + kTok - 1) / kTok;
+    out.r.T8 = (out.r.n8 + kTok - 1) / kTok;
+    out.r.b0 = __shfl_sync(kFull, i.b0, src);
+    out.r.nb = __shfl_sync(kFull, i.nb, src);
+    out.r.mt = __shfl_sync(kFull, i.mt, src);
+    return out;
 }
 
-// This CTA's run: a block scan over the rows (threads own contiguous ones), then the thread
-// whose rows hold the run's first place hands over where that is.
+// The same for any number: a block scan over the rows (threads own contiguous ones), then the
+// thread whose rows hold the run's first place hands over where that is.
 template <int D>
-__device__ __forceinline__ void schedule(const AttnArgs& a, char* smem) {
+__device__ __noinline__ void schedule_block(const AttnArgs& a, char* smem) {
     using L = Smem<D>;
     Sched* out = reinterpret_cast<Sched*>(smem + L::kSched);
     int2* sums = reinterpret_cast<int2*>(smem + L::kSums);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.p.d.R;
     const int per = (R + kThreads - 1) / kThreads, r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    RowInfo first{};
     int2 x = make_int2(0, 0);
     for (int r = r0; r < r1; ++r) {
         const RowInfo i = row_info(a, r);
-        if (r == r0) first = i;
         x.x += i.mt * unit_len(i);
         x.y += i.mt;
     }
     const int2 s = warp_scan(x);
     if (lane == 31) sums[warp] = s;
-    if (tid == 0) out->v = out->v_end = 0;
+    if (tid == 0) *out = Sched{};
     __syncthreads();
     int V = 0, at = s.x - x.x, units = s.y - x.y;
     for (int i = 0; i < kWarps; ++i) {
@@ -748,19 +779,15 @@ __device__ __forceinline__ void schedule(const AttnArgs& a, char* smem) {
             units += z.y;
         }
     }
-    if (V > 0 && r0 < r1) {
-        const Runs runs(V, gridDim.x);
-        if ((int)blockIdx.x < runs.P) {
-            const int v0 = runs.begin(blockIdx.x);
-            if (v0 >= at && v0 < at + x.x) {
-                for (int r = r0; r < r1; ++r) {
-                    const RowInfo i = r == r0 ? first : row_info(a, r);
-                    const int n = i.mt * unit_len(i);
-                    if (v0 >= at && v0 < at + n) *out = Sched{v0, runs.begin(blockIdx.x + 1), at, r, units, i};
-                    at += n;
-                    units += i.mt;
-                }
-            }
+    const Runs runs(V, gridDim.x, a.div_ctas);
+    if ((int)blockIdx.x < runs.P) {
+        const int v0 = runs.begin(blockIdx.x);
+        for (int r = r0; r < r1 && at <= v0; ++r) {
+            const RowInfo i = row_info(a, r);
+            const int n = i.mt * unit_len(i);
+            if (v0 < at + n) *out = Sched{v0, runs.begin(blockIdx.x + 1), at, r, units, i};
+            at += n;
+            units += i.mt;
         }
     }
     __syncthreads();
@@ -798,12 +825,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
         prefetch_map(&a.tm_v8);
     }
-    if (!a.p.early_start) pdl_wait();
-    schedule<D>(a, smem);
-    const Sched sched = *reinterpret_cast<const Sched*>(smem + L::kSched);
+    // (a prefetch reads nothing that the kernel uses)
+    if (warp == 0) {
+        const int r = min(lane, a.p.d.R - 1);
+        prefetch_l2(a.p.c.n_bf16 + r);
+        prefetch_l2(a.p.c.n_fp8 + r);
+        if (a.p.branch_start) prefetch_l2(a.p.branch_start + divided(r, a.div_hkv));
+    }
+    fence_before();
+    __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+    if (!a.p.early_start) pdl_wait();
+    Sched sched;
+    if (a.p.d.R <= 32) {
+        sched = schedule_warp(a);
+    } else {
+        schedule_block<D>(a, smem);
+        sched = *reinterpret_cast<const Sched*>(smem + L::kSched);
+    }
     if (sched.v < sched.v_end) {   // the same for the whole CTA
+        // registers go to the softmax warpgroups: 80 + 2 x 72 + 2 x 128 = the 5 x 96 at launch
+        if (warp < 4) set_regs<80, false>();
         if (warp == 0) {
             if (lane == 0) produce<D>(a, cx, base, Walk(a, sched));
         } else if (warp == 1) {
@@ -812,20 +855,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
                 multiply<D>(a, cx, base, tmem, Walk(a, sched));
             }
         } else if (warp >= 16) {
+            set_regs<72, false>();
             pdl_wait();
             convert<D, FMT, 1>(a, cx, smem, tid - 512, Walk(a, sched));
         } else if (warp >= 12) {
+            set_regs<72, false>();
             pdl_wait();
             convert<D, FMT, 0>(a, cx, smem, tid - 384, Walk(a, sched));
         } else if (warp >= 4) {
+            set_regs<128, true>();
             pdl_wait();
             softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2, Walk(a, sched), blockIdx.x);
         }
     }
-    if (blockIdx.x == 0 && warp == 3) {   // the workspace is the previous call's until it has finished
-        pdl_wait();
-        write_starts(a);
-    }
+    if (blockIdx.x == 0 && warp == 3) pdl_wait();   // the grid outlasts the previous kernel even with nothing to do
     __syncwarp();
     fence_before();
     __syncthreads();
@@ -840,84 +883,74 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 // of the row in CTA order and the own part, joined in float32; o is rounded to bf16.  The
 // loads of a batch of partials are all in flight at once.
 template <int D>
-__global__ void __launch_bounds__(D) prefix_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
-    constexpr int kBatch = 12;
+__global__ void __launch_bounds__(D) prefix_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kBatch = 10;
     const LayerDims& d = a.p.d;
     const int jq = threadIdx.x & 3, c4 = threadIdx.x >> 2;
-    const int b = blockIdx.x / d.hkv, g = blockIdx.x - b * d.hkv;
+    const int b = divided(blockIdx.x, a.div_hkv), g = blockIdx.x - b * d.hkv;
     pdl_launch_dependents();
     pdl_wait();
     if (jq >= d.G) return;
     const size_t mi = (size_t)blockIdx.x * 4 + jq, at = (((size_t)b * d.hq + g * d.G + jq) * D) / 4 + c4;
     float2 own = make_float2(kNegInf, 0.f);
-    float4 o_own = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.p.ml_own) {
         own = a.p.ml_own[mi];
-        o_own = reinterpret_cast<const float4*>(a.p.o_own)[at];
+        acc = reinterpret_cast<const float4*>(a.p.o_own)[at];
     }
     int pre = 0, b0 = 0;
     bool has = true;
     if (a.p.branch_start) {   // the last prefix that starts at or before b
-        int lo = 0, hi = d.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(a.p.branch_start + mid) <= b) lo = mid;
+        int hi = d.batch;
+        while (hi - pre > 1) {
+            const int mid = (pre + hi) / 2;
+            if (__ldg(a.p.branch_start + mid) <= b) pre = mid;
             else hi = mid;
         }
-        pre = lo;
-        const int s = __ldg(a.p.branch_start + pre);
-        has = s <= b && b < __ldg(a.p.branch_start + pre + 1);
-        b0 = max(s, 0);
+        b0 = __ldg(a.p.branch_start + pre);
+        has = b0 <= b && b < __ldg(a.p.branch_start + pre + 1);
+        b0 = max(b0, 0);
     }
-    float M = kNegInf, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (own.y != 0.f) {   // L = 0: no own tokens
-        M = own.x;
-        L = own.y;
-        acc = make_float4(L * o_own.x, L * o_own.y, L * o_own.z, L * o_own.w);
-    }
+    const int row = pre * d.hkv + g, m = divided(b - b0, a.div_unit);
+    const int in_unit = b - b0 - m * a.row_tiles * a.per_tile, rt = in_unit >= a.per_tile;
+    const int rr = (in_unit - rt * a.per_tile) * d.G + jq;
+    int2 slots = make_int2(0, -1);
     if (has) {
-        const int row = pre * d.hkv + g;
-        const Runs runs(a.starts[d.R].x, ctas);
-        const int2 st = a.starts[row];
-        const RowInfo r = row_info(a, row);
-        const int len = unit_len(r);
-        if (len > 0) {
-            const int per_unit = a.row_tiles * a.per_tile, m = (b - b0) / per_unit, in_unit = b - b0 - m * per_unit;
-            const int rt = in_unit / a.per_tile, rr = (in_unit - rt * a.per_tile) * d.G + jq;
-            const int v = st.x + m * len, c0 = runs.of(v + kSegCost), c1 = runs.of(v + len - 1), unit = st.y + m;
-            auto slot = [&](int c) { return (size_t)min(c + unit, a.slots - 1) * a.row_tiles + rt; };
-            for (int c = c0; c <= c1; c += kBatch) {
-                float2 ml[kBatch];
-                float4 x[kBatch];
+        slots = __ldcg(a.unit_slots + (size_t)row * a.row_units + min(m, a.row_units - 1));
+        if (min(__ldg(a.p.c.n_bf16 + row), d.cap_o) <= 0 && min(__ldg(a.p.c.n_fp8 + row), d.cap_q) <= 0) slots.y = -1;
+        slots.x = max(slots.x, 0);
+        slots.y = min(slots.y, a.slots - 1);
+    }
+    const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
+    float M = own.y != 0.f ? own.x : kNegInf, L = own.y;   // L = 0: no own tokens
+    acc = own.y != 0.f ? make_float4(L * acc.x, L * acc.y, L * acc.z, L * acc.w) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = slots.x; c <= slots.y; c += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
 #pragma unroll
-                for (int q = 0; q < kBatch; ++q) {
-                    ml[q] = make_float2(kNegInf, 0.f);
-                    x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + q <= c1) {
-                        const size_t s = slot(c + q);
-                        ml[q] = __ldcg(a.part_ml + s * kRows + rr);
-                        x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + rr);
-                    }
-                }
-                float mb = M;
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, ml[q].y != 0.f ? ml[q].x : kNegInf);
-                if (mb > M) {
-                    const float f = M == kNegInf ? 0.f : exp_scaled(M, mb, a.p.inv_sqrt_d);
-                    L *= f;
-                    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-                    M = mb;
-                }
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q) {
-                    if (ml[q].y == 0.f) continue;   // a partial without weight; a NaN goes through
-                    const float f = ml[q].x == M ? 1.f : exp_scaled(ml[q].x, M, a.p.inv_sqrt_d);
-                    L = fmaf(ml[q].y, f, L);
-                    acc.x = fmaf(x[q].x, f, acc.x); acc.y = fmaf(x[q].y, f, acc.y);
-                    acc.z = fmaf(x[q].z, f, acc.z); acc.w = fmaf(x[q].w, f, acc.w);
-                }
+        for (int q = 0; q < kBatch; ++q) {
+            ml[q] = make_float2(kNegInf, 0.f);
+            if (c + q <= slots.y) {
+                const size_t s = (size_t)(c + q) * a.row_tiles + rt;
+                ml[q] = __ldcg(a.part_ml + s * kRows + rr);
+                x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + rr);
             }
+        }
+        float mb = M;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, ml[q].y != 0.f ? ml[q].x : kNegInf);
+        // differences are small where a weight counts, so float32 keeps them
+        const float f = M == mb ? 1.f : ex2((M - mb) * c2);
+        M = mb;
+        L *= f;
+        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            if (ml[q].y == 0.f) continue;   // no weight (a NaN goes through)
+            const float w = ml[q].x == M ? 1.f : ex2((ml[q].x - M) * c2);
+            L = fmaf(ml[q].y, w, L);
+            acc.x = fmaf(x[q].x, w, acc.x); acc.y = fmaf(x[q].y, w, acc.y);
+            acc.z = fmaf(x[q].z, w, acc.z); acc.w = fmaf(x[q].w, w, acc.w);
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -967,9 +1000,9 @@ bool make_q_map(CUtensorMap* m, const void* base, const LayerDims& d, int branch
 }
 
 struct PrefixWs {
-    size_t part_o, part_ml, starts, total;
+    size_t part_o, part_ml, unit_slots, total;
     long long slots, units, places;
-    int per_tile, row_tiles;
+    int per_tile, row_tiles, row_units;
 };
 
 // A segment's partial goes to slot (CTA + unit): along the list each next segment raises one
@@ -979,13 +1012,14 @@ PrefixWs ws_layout(const LayerDims& d, int branches) {
     PrefixWs w{};
     w.per_tile = kRows / d.G;
     w.row_tiles = branches > w.per_tile ? 2 : 1;
+    w.row_units = (branches + w.row_tiles * w.per_tile - 1) / (w.row_tiles * w.per_tile);
     w.units = (long long)d.hkv * (d.batch + branches / (w.row_tiles * w.per_tile));
     w.places = w.units * (((long long)d.cap_o + kTok - 1) / kTok + ((long long)d.cap_q + kTok - 1) / kTok + kSegCost);
     w.slots = kMaxCtas + w.units;
     auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
     const size_t rows = (size_t)w.slots * w.row_tiles * kRows;
     size_t off = 0;
-    w.starts = off;  off = al(off + sizeof(int2) * ((size_t)d.R + 1));
+    w.unit_slots = off; off = al(off + sizeof(int2) * (size_t)d.R * w.row_units);
     w.part_ml = off; off = al(off + sizeof(float2) * rows);
     w.part_o = off;  off = al(off + sizeof(float) * rows * d.D);
     w.total = off;
@@ -1000,13 +1034,17 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     const LayerDims& d = p.d;
     const PrefixWs w = ws_layout(d, p.branches);
     const long long blocks = (long long)p.branches * d.hkv;
-    if (w.places > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const long long per_unit = (long long)w.row_tiles * w.per_tile;
+    if (w.places > 0x7fffffff || blocks * d.hkv > 0xffffffffll || (long long)d.R * d.hkv > 0xffffffffll ||
+        (p.branches + per_unit) * per_unit > 0xffffffffll)
+        return cudaErrorInvalidValue;
     AttnArgs a{};
     a.p = p;
     a.slots = (int)w.slots;
     a.per_tile = w.per_tile;
     a.row_tiles = w.row_tiles;
-    a.starts = reinterpret_cast<int2*>((char*)ws + w.starts);
+    a.unit_slots = reinterpret_cast<int2*>((char*)ws + w.unit_slots);
+    a.row_units = w.row_units;
     a.part_ml = reinterpret_cast<float2*>((char*)ws + w.part_ml);
     a.part_o = reinterpret_cast<float4*>((char*)ws + w.part_o);
     const long long r16 = (long long)d.R * d.cap_o, r8 = (long long)d.R * d.cap_q;
@@ -1020,7 +1058,11 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     long long ctas = sms < kMaxCtas ? sms : kMaxCtas;   // one an SM
     if (ctas > w.places) ctas = w.places;
-    static unsigned char done[4][64];
+    auto divisor = [](long long x) { return x == 1 ? 0u : (unsigned)(0x100000000ll / x + 1); };
+    a.div_hkv = divisor(d.hkv);
+    a.div_unit = divisor(per_unit);
+    a.div_ctas = divisor(ctas);
+    static unsigned char done[4][64], done_join[4][64];
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1029,7 +1071,10 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     lc.attrs = attr;
     lc.numAttrs = 1;
     auto go = [&](auto kernel, auto join, int which, int bytes) {
+        // both with the largest shared-memory carveout: an SM runs them side by side only if it
+        // need not change its split between them
         cudaError_t err = allow_max_dyn_smem(kernel, done[which]);
+        if (err == cudaSuccess) err = allow_max_dyn_smem(join, done_join[which]);
         if (err != cudaSuccess) return err;
         lc.gridDim = dim3((unsigned)ctas);
         lc.blockDim = dim3(kThreads);
@@ -1038,7 +1083,7 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
         lc.gridDim = dim3((unsigned)blocks);
         lc.blockDim = dim3((unsigned)d.D);
         lc.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&lc, join, a, (int)ctas);
+        return cudaLaunchKernelEx(&lc, join, a);
     };
     if (d.D == 128)
         e = d.fmt == ARKV_FMT_E5M2
