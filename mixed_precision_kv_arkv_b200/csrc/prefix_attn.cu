@@ -15,11 +15,12 @@
 // that the run that holds them has that many tiles less.
 // prefix_join_kernel joins the partials and the branch's own part.
 //
-// A CTA: warp 0 streams K and V by TMA through a ring of slots (a slot is a tile's K or
-// its V), warp 1 issues the products, two warpgroups do the softmax (thread = row =
-// tensor-memory lane), each with its own S, P and O in tensor memory and its own state, so
-// that neither waits for the other, and two warpgroups rewrite FP8 tiles in place as bf16
-// (exact: 4 or 3 significant bits), one K, one V.  With one tile of rows the softmax
+// A CTA: warp 3 walks the run and hands its segments to the others through shared memory,
+// warp 0 streams K and V by TMA through a ring of slots (a slot is a tile's K or its V),
+// warp 1 issues the products, two warpgroups do the softmax, each with its own S, P and O
+// in tensor memory and its own state, so that neither waits for the other, and two
+// warpgroups rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits), one K,
+// one V.  With one tile of rows the softmax
 // warpgroups take the token tiles in turn and their two O are added at the end of the
 // segment; with two each has its rows, and a token tile is loaded and converted once for
 // both.  Either way a softmax job is one S, and the jobs alternate.
@@ -27,7 +28,7 @@
 // scale is folded into P.  The softmax reference m moves only when a logit exceeds it by
 // 2^8, so O is seldom rescaled.  P is rounded to bf16 once, the rounding that o itself
 // gets; the sum is of the unrounded values.
-// The loops over a tile's columns are not unrolled past 32: a short call runs each piece of
+// The loops over a tile's columns are not unrolled past 16: a short call runs each piece of
 // code once or twice, and fetching it cost more than the arithmetic.
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
@@ -67,10 +68,20 @@ struct Sched {
     RowInfo r;
 };
 
+// A segment: tiles [i, i_end) of a unit of T tiles, T8 of them FP8, and the interleave's
+// state at tile i (f8 FP8 tiles before it).
+enum : int { kSegFirst = 1, kSegLast = 2, kSegTwo = 4, kSegEnd = 8 };
+struct Seg {
+    int row, n16, n8, T, T8, i, i_end, f8, err;
+    int branch, rows0, rows1;   // first branch; live rows of the two tiles of rows
+    int slot, flags;            // place of its partial; first, last of its unit, two tiles of rows, no segment
+};
+
 // ------------------------------------------------------------------ shared memory
 template <int D>
 struct Smem {
     static constexpr int kSlots = 5;
+    static constexpr int kSegs = 2;                         // segments on their way from the scheduler
     static constexpr int kSlot = kTok * D * 2;              // a K or V tile in bf16
     static constexpr int kRegion = kTok * 128;              // 64 dimensions of it (128-byte rows, swizzled)
     static constexpr int kRaw = D == 64 ? kSlot / 2 : 0;    // where in its slot an FP8 tile lands
@@ -85,12 +96,13 @@ struct Smem {
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
                          kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 2, kScFull = kPFull + 2,
                          kScFree = kScFull + 2, kOFull = kScFree + 2, kXch = kOFull + 1, kEpi = kXch + 1,
-                         kFin = kEpi + 1, kCvt = kFin + 1, kNumBars = kCvt + 2;
+                         kFin = kEpi + 1, kCvt = kFin + 1, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
+                         kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
-    static constexpr int kSched = kMisc + 16;
-    static constexpr int kSums = kSched + 64;                           // int2 [kWarps]: the scan's warp sums
-    static constexpr int kBytes = kSums + kWarps * 8;
-    static_assert(sizeof(Sched) <= 64 && kBytes <= 232448, "shared memory of one CTA");
+    static constexpr int kSeg = kMisc + 16;                             // Seg [kSegs]
+    static constexpr int kSums = kSeg + kSegs * 64;                     // int2 [32]: scan of the rows
+    static constexpr int kBytes = kSums + 32 * 8;
+    static_assert(sizeof(Seg) <= 64 && kBytes <= 232448, "shared memory of one CTA");
 };
 
 // tensor-memory columns: S (and P) of the two warpgroups, then their O
@@ -106,8 +118,7 @@ struct AttnArgs {
     PrefixParams p;
     float4* part_o;      // [slots][row_tiles][D / 4][128 rows]: a warp's rows side by side
     float2* part_ml;     // [slots][row_tiles][128]
-    int2* unit_slots;    // [R][row_units]: the first and last slot with a partial of a unit
-    int row_units;       // units of a row, at most
+    int4* join;          // [branches][hkv]: first and last slot with a partial, row in it (none: last < first)
     unsigned div_hkv, div_unit, div_ctas;   // divisors hkv, branches of a unit, CTAs (see divided)
     int slots;
     int per_tile;        // branches of one tile of rows
@@ -160,74 +171,29 @@ struct Runs {
 };
 
 struct Tile {
-    int fp8, idx, valid;   // kind, place in its segment, live tokens
+    int fp8, idx, valid;   // kind, place in its row's segment of the cache, live tokens
 };
 
-// Walks a CTA's run: segments (the run's tiles of one unit), then their tiles.
-struct Walk {
-    const AttnArgs& a;
-    int v, v_end, base;         // next place, end of the run, first place of the unit
-    int row, m, unit0;          // the unit: row, place in it; units before the row
-    RowInfo r;
-    int T, i, i_end, err, f8;   // tiles of the unit; next tile and end of the segment; the interleave
-
-    __device__ __forceinline__ Walk(const AttnArgs& args, const Sched& s)
-        : a(args), v(s.v), v_end(s.v_end), base(s.base), row(s.row), m(0), unit0(s.units), r(s.r), T(r.T16 + r.T8), i(0),
-          i_end(0), err(0), f8(0) {
-        if (r.mt > 1) {
-            m = (v - base) / (T + kSegCost);
-            base += m * (T + kSegCost);
-        }
-    }
-    __device__ __forceinline__ bool segment() {
-        while (v < v_end) {
-            while (v >= base + T + kSegCost) {
-                base += T + kSegCost;
-                if (++m >= r.mt) {
-                    do {
-                        unit0 += r.mt;
-                        if (++row >= a.p.d.R) return false;
-                        r = row_info(a, row);
-                        T = r.T16 + r.T8;
-                    } while (T == 0 || r.mt == 0);
-                    m = 0;
-                }
-            }
-            i = max(v - base - kSegCost, 0);
-            i_end = min(v_end - base - kSegCost, T);
-            v = min(base + kSegCost + T, v_end);
-            if (i < i_end) {   // after i tiles, floor(i T8 / T) are FP8
-                if (T < 65536) {
-                    const unsigned w = (unsigned)i * r.T8;
-                    f8 = w / (unsigned)T;
-                    err = w - f8 * T;
-                } else {
-                    const long long w = (long long)i * r.T8;
-                    f8 = (int)(w / T);
-                    err = (int)(w - (long long)f8 * T);
-                }
-                return true;
-            }
-        }
-        return false;
-    }
-    __device__ __forceinline__ Tile tile() {
+// The tiles of a segment in order: after i tiles of a unit, floor(i T8 / T) are FP8.
+struct Tiles {
+    int i, n16, n8, T, T8, f8, err;
+    __device__ __forceinline__ explicit Tiles(const Seg& s)
+        : i(s.i), n16(s.n16), n8(s.n8), T(s.T), T8(s.T8), f8(s.f8), err(s.err) {}
+    __device__ __forceinline__ Tile next() {
         Tile x;
-        err += r.T8;
+        err += T8;
         x.fp8 = err >= T;
         if (x.fp8) {
             err -= T;
             x.idx = f8++;
-            x.valid = min(kTok, r.n8 - x.idx * kTok);
+            x.valid = min(kTok, n8 - x.idx * kTok);
         } else {
             x.idx = i - f8;
-            x.valid = min(kTok, r.n16 - x.idx * kTok);
+            x.valid = min(kTok, n16 - x.idx * kTok);
         }
         ++i;
         return x;
     }
-    __device__ __forceinline__ int first_branch() const { return m * a.row_tiles * a.per_tile; }   // of the prefix's
-    __device__ __forceinline__ bool two() const { return r.nb - first_branch() > a.per_tile; }     // tiles of rows
 };
 
 // ------------------------------------------------------------------ helpers
@@ -250,6 +216,28 @@ struct Ctx {
     // The same for a whole warp, with one outcome.
     __device__ __forceinline__ bool warp_wait(int i, uint32_t parity) const { return __all_sync(kFull, wait(i, parity)); }
 };
+
+// Segment number `seg` from the scheduler (one thread); false at the end of the run.
+template <int D>
+__device__ __forceinline__ bool thread_segment(const Ctx& cx, const char* smem, int seg, Seg& out) {
+    using L = Smem<D>;
+    const int z = seg % L::kSegs;
+    if (!cx.wait(L::kSegFull + z, (seg / L::kSegs) & 1)) return false;
+    out = *reinterpret_cast<const Seg*>(smem + L::kSeg + z * 64);
+    mbar_arrive(cx.bar(L::kSegEmpty + z));
+    return !(out.flags & kSegEnd);
+}
+// The same for a warp.
+template <int D>
+__device__ __forceinline__ bool warp_segment(const Ctx& cx, const char* smem, int seg, Seg& out) {
+    using L = Smem<D>;
+    const int z = seg % L::kSegs;
+    if (!cx.warp_wait(L::kSegFull + z, (seg / L::kSegs) & 1)) return false;
+    out = *reinterpret_cast<const Seg*>(smem + L::kSeg + z * 64);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bar(L::kSegEmpty + z));
+    return !(out.flags & kSegEnd);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -284,13 +272,14 @@ __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 6
 
 // ------------------------------------------------------------------ producer (one thread)
 template <int D>
-__device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w) {
+__device__ void produce(const AttnArgs& a, const Ctx& cx, const char* gsmem, uint32_t smem) {
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     int e = 0, seg = 0;
     uint32_t ph[3] = {0, 0, 0}, last[3] = {0, 0, 0};   // by barrier (full, raw K, raw V): parity of each slot's next
                                                        // phase, the slots whose last load it has
     bool ok = true, waited = !a.p.early_start;
+    Seg w{};
     auto load = [&](const Tile& x, bool v) {
         const int s = e % L::kSlots;
         if (e >= L::kSlots && !cx.wait(L::kEmptyB + s, ((e / L::kSlots) & 1) ^ 1)) return false;
@@ -315,13 +304,14 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w)
         ++e;
         return true;
     };
-    while (ok && w.segment()) {
+    while (ok && thread_segment<D>(cx, gsmem, seg, w)) {
+        Tiles tiles(w);
         // The segment's queries follow its first tiles: an early-started call fills its whole
         // ring before the wait for the previous kernel, and a later segment's queries wait
         // until the products of the one before have read theirs, which its first tile need not.
         const int n = w.i_end - w.i, ahead = min(n, seg == 0 && a.p.early_start ? L::kSlots / 2 : 1);
         for (int j = 0; ok && j < n; ++j) {
-            const Tile x = w.tile();
+            const Tile x = tiles.next();
             ok = load(x, false) && load(x, true);
             if (!ok || j != ahead - 1) continue;
             if (!waited) {
@@ -329,13 +319,13 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w)
                 waited = true;
             }
             if (seg > 0 && !(ok = cx.wait(L::kQEmpty, (seg - 1) & 1))) continue;
-            const int tiles = w.two() ? 2 : 1, b0 = w.r.b0 + w.first_branch();
-            mbar_expect_tx(cx.bar(L::kQFull), tiles * a.per_tile * d.G * D * 2);
-            for (int t = 0; t < tiles; ++t)
+            const int count = w.flags & kSegTwo ? 2 : 1;
+            mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
+            for (int t = 0; t < count; ++t)
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                     tma_load_4d(smem + L::kQ + t * L::kQTile + c * L::kRegion, &a.tm_q, 64 * c, 0, w.row % d.hkv,
-                                b0 + t * a.per_tile, cx.bar(L::kQFull));
+                                w.branch + t * a.per_tile, cx.bar(L::kQFull));
             ++seg;
         }
     }
@@ -357,7 +347,7 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, uint32_t smem, Walk w)
 // rows, token tile x / 2 with two.  S of job x + 1 is issued before P V of job x, and so
 // after that of job x - 1, which read P from the same place.
 template <int D>
-__device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32_t tmem, Walk w) {
+__device__ void multiply(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false), kIdPV = idesc_bf16(kRows, D, true);
     int j = 0, seg = 0;            // tiles and segments so far
@@ -372,8 +362,10 @@ __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32
         ph ^= 1u << s;
         return r;
     };
-    while (ok && w.segment()) {
-        const bool two = w.two();
+    Seg w;
+    while (ok && thread_segment<D>(cx, gsmem, seg, w)) {
+        Tiles tiles(w);
+        const bool two = w.flags & kSegTwo;
         const int sh = two ? 1 : 0, n = w.i_end - w.i, jobs = n << sh;
         ok = cx.wait(L::kQFull, seg & 1) && (seg == 0 || cx.wait(L::kEpi, (seg - 1) & 1));
         uint32_t conv_v = 0;       // by job & 1: its V tile is converted
@@ -383,7 +375,7 @@ __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32
                 const int b = x & 1, e = 2 * (j + (x >> sh)), s = e % L::kSlots;
                 const bool opens = !two || b == 0, closes = !two || b == 1;   // the tile's first, last job
                 if (opens) {
-                    t = w.tile();
+                    t = tiles.next();
                     if (!(ok = ready(e, t.fp8))) break;
                     fence_after();
                 }
@@ -425,53 +417,49 @@ __device__ void multiply(const AttnArgs& a, const Ctx& cx, uint32_t smem, uint32
 }
 
 // ------------------------------------------------------------------ FP8 -> bf16 (128 threads, one a token)
-// KV = 0: the K tiles and the scales, 1: the V tiles, whose rows past the segment end
+// kv = 0: the K tiles and the scales, 1: the V tiles, whose rows past the segment end
 // become zero in either format (stale bits must not meet P = 0).
-template <int D, int FMT, int KV>
-__device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, Walk w) {
+template <int D, int FMT>
+__device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, int kv) {
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
     float* scales = reinterpret_cast<float*>(smem + L::kScale);
-    int cvt = 0, f = 0;      // uses of the read-before-write barrier (D = 64); FP8 tiles so far
-    uint32_t raw_ph = 0;     // parity of each slot's next phase (of the K or V loads to convert)
-    auto next = [&](Tile& x) {
-        if (w.i == w.i_end && !w.segment()) return false;
-        x = w.tile();
-        return true;
-    };
-    auto load_scales = [&](const Tile& x, int row, float& sk, float& sv) {
-        sk = 1.f;            // past the segment end: a masked column
-        sv = 0.f;
-        if (KV == 0 && x.fp8 && ct < x.valid) {
-            const size_t at = (size_t)row * d.cap_q + x.idx * kTok + ct;
-            sk = __ldg(a.p.c.sk + at) * c2;
-            sv = __ldg(a.p.c.sv + at);
-        }
-    };
-    Tile cur{}, ahead{};
-    float sk, sv, sk1 = 0.f, sv1 = 0.f;
-    if (!next(cur)) return;
-    load_scales(cur, w.row, sk, sv);
+    int cvt = 0, f = 0, j = 0;   // uses of the read-before-write barrier (D = 64); FP8 tiles, tiles so far
+    uint32_t raw_ph = 0;         // parity of each slot's next phase (of the K or V loads to convert)
+    Seg w;
+    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
+        Tiles tiles(w);
+        float sk = 1.f, sv = 0.f;   // of this thread's token in the segment's next FP8 tile
+        auto load_scales = [&](int idx) {
+            const int t = idx * kTok + ct;
+            sk = 1.f;               // past the end: a masked column
+            sv = 0.f;
+            if (kv == 0 && t < w.n8) {
+                sk = __ldg(a.p.c.sk + (size_t)w.row * d.cap_q + t) * c2;
+                sv = __ldg(a.p.c.sv + (size_t)w.row * d.cap_q + t);
+            }
+        };
+        load_scales(w.f8);
 #pragma unroll 1
-    for (int j = 0;; ++j) {
-        const bool more = next(ahead);   // the next tile's scales are loaded one tile early
-        if (more) load_scales(ahead, w.row, sk1, sv1);
-        const int s = (2 * j + KV) % L::kSlots;
-        const bool tail = KV == 1 && !cur.fp8 && cur.valid < kTok;
-        if (cur.fp8 || tail) {
-            if (KV == 0) {
+        for (const int end = w.i_end; tiles.i < end; ++j) {
+            const Tile cur = tiles.next();
+            const int s = (2 * j + kv) % L::kSlots;
+            const bool tail = kv == 1 && !cur.fp8 && cur.valid < kTok;
+            if (!cur.fp8 && !tail) continue;
+            if (kv == 0) {
                 const int z = f & 1, use = f >> 1;
                 if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // their last readers
                 scales[(2 * z) * kTok + ct] = sk;
                 scales[(2 * z + 1) * kTok + ct] = sv;
                 mbar_arrive(cx.bar(L::kScFull + z));
                 ++f;
+                load_scales(cur.idx + 1);   // the next ones, on their way during this tile
             }
-            if (!cx.warp_wait(L::kRawB + KV * L::kSlots + s, (raw_ph >> s) & 1u)) return;
+            if (!cx.warp_wait(L::kRawB + kv * L::kSlots + s, (raw_ph >> s) & 1u)) return;
             raw_ph ^= 1u << s;
             char* slot = smem + L::kRing + s * L::kSlot;
-            const bool zero = KV == 1 && ct >= cur.valid;
+            const bool zero = kv == 1 && ct >= cur.valid;
             if (!tail) {
                 // 64 dimensions at a time, the upper half of a 128-byte row first: the codes lie
                 // where the lower half goes
@@ -485,8 +473,8 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, Wa
                         if (zero) raw[c] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     if constexpr (D == 64) {   // rows grow over other threads' codes (D = 128: over their own alone)
-                        mbar_arrive(cx.bar(L::kCvt + KV));
-                        if (!cx.warp_wait(L::kCvt + KV, cvt++ & 1)) return;
+                        mbar_arrive(cx.bar(L::kCvt + kv));
+                        if (!cx.warp_wait(L::kCvt + kv, cvt++ & 1)) return;
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -501,7 +489,7 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, Wa
                     }
                 }
             } else if (zero) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 8; ++c)
                     *reinterpret_cast<uint4*>(slot + (c >> 3) * L::kRegion + ct * 128 + ((c & 7) << 4)) =
                         make_uint4(0u, 0u, 0u, 0u);
@@ -509,129 +497,183 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, Wa
             fence_proxy_async();
             mbar_arrive(cx.bar(L::kConvB + s));
         }
-        if (!more) return;
-        cur = ahead;
-        sk = sk1;
-        sv = sv1;
     }
 }
 
-// ------------------------------------------------------------------ softmax (128 threads, one a row)
-// Row state in log2 units (logit * log2(e) / sqrt(D)): the reference m of P and O, the
-// largest logit top, the sum l of 2^(x - m).
-struct Row {
-    float m, top, l;
+// ------------------------------------------------------------------ softmax (128 threads)
+// A warp owns 32 rows (tensor-memory lanes).  S is read in the matrix layout: lane t holds of
+// rows t / 4 + 8 k (k = 0..3) the columns 2 (t % 4), 2 (t % 4) + 1 of every 8, so that the
+// per-column FP8 scales are read once for four rows (a lane a row, every lane reads every
+// scale, and the shared memory's bandwidth set the time: 3.1 us a job against 1.9).
+// State of a lane's rows in log2 units (logit * log2(e) / sqrt(D)): the reference m of P
+// and O (the same in the four lanes of a row), the largest logit top and the sum l of
+// 2^(x - m), both of this lane's columns alone.
+struct Rows {
+    float m[4], top[4], l[4];
 };
 
-// Sixteen columns of S: those from `valid` on are no tokens; times their K scales (FP8).
+// 16 columns of S from column s on, times their K scales (FP8); columns from `valid` on are
+// no tokens.  v[k][2 g + e]: row k, column 8 g + 2 (t % 4) + e.
 template <bool FP8>
-__device__ __forceinline__ void logits16(float (&v)[16], int valid, const float* sk) {
-    float4 k[4];
+__device__ __forceinline__ void logits16(uint32_t s, int valid, const float* sk, float2 (&v)[4][2]) {
+    float2 k[2];
+    const int col = 2 * (threadIdx.x & 3);
     if (FP8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = reinterpret_cast<const float4*>(sk)[i];
+        k[0] = *reinterpret_cast<const float2*>(sk + col);
+        k[1] = *reinterpret_cast<const float2*>(sk + 8 + col);
     }
-    wait_ld(v);
+    float a[8], b[8];
+    tmem_ld_16x256b_x2(s, a);
+    tmem_ld_16x256b_x2(s + (16u << 16), b);
+    wait_ld(a, b);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        v[0][g] = make_float2(a[4 * g], a[4 * g + 1]);
+        v[1][g] = make_float2(a[4 * g + 2], a[4 * g + 3]);
+        v[2][g] = make_float2(b[4 * g], b[4 * g + 1]);
+        v[3][g] = make_float2(b[4 * g + 2], b[4 * g + 3]);
+    }
     if (valid < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i >= valid) v[i] = kNegInf;
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (8 * g + col >= valid) v[r][g].x = kNegInf;
+                if (8 * g + col + 1 >= valid) v[r][g].y = kNegInf;
+            }
     }
     if (FP8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = mul2(make_float2(v[4 * i], v[4 * i + 1]), make_float2(k[i].x, k[i].y));
-            const float2 y = mul2(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(k[i].z, k[i].w));
-            v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = y.x; v[4 * i + 3] = y.y;
-        }
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r][g] = mul2(v[r][g], k[g]);
     }
 }
 
-// One job: S at column s of this thread's lane becomes P.  O (column o) is idle while it
+// Over the four lanes of a row.
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+    return fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(kFull, x, 1);
+    return x + __shfl_xor_sync(kFull, x, 2);
+}
+// From the matrix layout to a lane a row: the value of row `lane`.
+__device__ __forceinline__ float row_value(const float (&x)[4]) {
+    const int lane = threadIdx.x & 31, src = 4 * (lane & 7);
+    const float y0 = __shfl_sync(kFull, x[0], src), y1 = __shfl_sync(kFull, x[1], src);
+    const float y2 = __shfl_sync(kFull, x[2], src), y3 = __shfl_sync(kFull, x[3], src);
+    return lane < 16 ? (lane < 8 ? y0 : y1) : (lane < 24 ? y2 : y3);
+}
+
+// One job: S at column s of the warp's lanes becomes P.  O (column o) is idle while it
 // lasts: the product into S came after the last one into O.  S is read twice, 16 columns at
 // a time.
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
-                                            const float* sv, float c2, Row& r) {
-    float v[16];
+                                            const float* sv, float c2, Rows& r) {
+    float2 v[4][2];
     float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll 1
     for (int c = 0; c < kTok; c += 16) {
-        tmem_ld16(s + c, v);
-        logits16<FP8>(v, valid - c, sk + c);
+        logits16<FP8>(s + c, valid - c, sk + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[i + e]), v[i + 4 + e]);
+        for (int k = 0; k < 4; ++k)
+            mx[k] = fmaxf(fmaxf(fmaxf(mx[k], v[k][0].x), fmaxf(v[k][0].y, v[k][1].x)), v[k][1].y);
     }
-    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    if (!FP8) top *= c2;
-    r.top = fmaxf(r.top, top);
-    if (first) {
-        r.m = top == kNegInf ? 0.f : top;
-    } else {
-        const bool move = top > r.m + 8.f;
-        if (__any_sync(kFull, move)) {
-            const float f = move ? ex2(r.m - top) : 1.f;
-            r.l *= f;
-            if (move) r.m = top;
+    bool move = first;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (!FP8) mx[k] *= c2;
+        r.top[k] = fmaxf(r.top[k], mx[k]);
+        move |= mx[k] > r.m[k] + 8.f;
+    }
+    if (__any_sync(kFull, move)) {
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float top = quad_max(mx[k]);
+            f[k] = 1.f;
+            if (first) {
+                r.m[k] = top == kNegInf ? 0.f : top;
+            } else if (top > r.m[k] + 8.f) {
+                f[k] = ex2(r.m[k] - top);
+                r.l[k] *= f[k];
+                r.m[k] = top;
+            }
+        }
+        if (!first) {
+            const float ff = row_value(f);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float x[32];
-                tmem_ld32(o + c, x);
+            for (int c = 0; c < D; c += 16) {
+                float x[16];
+                tmem_ld16(o + c, x);
                 wait_ld(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= f;
-                tmem_st32(o + c, x);
+                for (int i = 0; i < 16; ++i) x[i] *= ff;
+                tmem_st16(o + c, x);
             }
         }
     }
-    const float2 m2 = make_float2(-r.m, -r.m), cc = FP8 ? make_float2(1.f, 1.f) : make_float2(c2, c2);
-    float2 l = make_float2(0.f, 0.f);
+    const float2 cc = make_float2(c2, c2);
+    float2 l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l[k] = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int c = 0; c < kTok; c += 16) {
-        tmem_ld16(s + c, v);
-        logits16<FP8>(v, valid - c, sk + c);
-        uint32_t pk[8];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (FP8) f = *reinterpret_cast<const float4*>(sv + c + i);
-            float2 a = FP8 ? add2(make_float2(v[i], v[i + 1]), m2) : fma2(make_float2(v[i], v[i + 1]), cc, m2);
-            float2 b = FP8 ? add2(make_float2(v[i + 2], v[i + 3]), m2) : fma2(make_float2(v[i + 2], v[i + 3]), cc, m2);
-            a = make_float2(ex2(a.x), ex2(a.y));
-            b = make_float2(ex2(b.x), ex2(b.y));
-            l = add2(l, add2(a, b));
-            if (FP8) {
-                a = mul2(a, make_float2(f.x, f.y));
-                b = mul2(b, make_float2(f.z, f.w));
-            }
-            pk[i / 2] = pack_bf16(a.x, a.y);
-            pk[i / 2 + 1] = pack_bf16(b.x, b.y);
+        logits16<FP8>(s + c, valid - c, sk + c, v);
+        float2 f[2];
+        if (FP8) {
+            f[0] = *reinterpret_cast<const float2*>(sv + c + 2 * (threadIdx.x & 3));
+            f[1] = *reinterpret_cast<const float2*>(sv + c + 8 + 2 * (threadIdx.x & 3));
         }
-        tmem_st8(s + c / 2, pk);   // over columns of S that have been read
+        uint32_t lo[4], hi[4];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 m2 = make_float2(-r.m[k], -r.m[k]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                float2 p = FP8 ? add2(v[k][g], m2) : fma2(v[k][g], cc, m2);
+                p = make_float2(ex2(p.x), ex2(p.y));
+                l[k] = add2(l[k], p);
+                if (FP8) p = mul2(p, f[g]);
+                (k < 2 ? lo : hi)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
+            }
+        }
+        tmem_st_16x128b_x2(s + c / 2, lo);   // over columns of S that have been read
+        tmem_st_16x128b_x2(s + c / 2 + (16u << 16), hi);
     }
-    r.l += l.x + l.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.l[k] += l[k].x + l[k].y;
     wait_st();
 }
 
 template <int D>
-__device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t tmem, int b, Walk w, int cta) {
+__device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t tmem, int b) {
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b), o = lane + tmem_o<D>(b);
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    int seg = 0, f = 0, xch = 0;   // segments, FP8 tiles and exchanges so far
+    int f = 0, xch = 0;        // FP8 tiles and exchanges so far
     uint32_t s_ph = 0;         // parity of this warpgroup's next S
-    while (w.segment()) {
-        const bool two = w.two();
-        const int i0 = w.i, n = w.i_end - i0;
-        Row r{0.f, kNegInf, 0.f};
+    Seg w;
+    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
+        const bool two = w.flags & kSegTwo;
+        const int n = w.i_end - w.i;
+        Tiles tiles(w);
+        Rows r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            r.m[k] = 0.f;
+            r.top[k] = kNegInf;
+            r.l[k] = 0.f;
+        }
         bool first = true;
 #pragma unroll 1
         for (int x = 0; x < n; ++x) {
-            const Tile t = w.tile();
+            const Tile t = tiles.next();
             const int z = f & 1, use = (f >> 1) & 1;
             f += t.fp8;
             if (!two && (x & 1) != b) continue;
@@ -650,13 +692,20 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             mbar_arrive(cx.bar(L::kPFull + b));
             if (t.fp8) mbar_arrive_n(cx.bar(L::kScFree + z), two ? 1 : 2);   // 256 in all, whoever read them
         }
+        // The segment's partial, a lane a row from here.  With one tile of rows both warpgroups
+        // hold half of the tokens: each gets the other's state (through S, idle by then) and adds
+        // half of the columns.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            r.top[k] = quad_max(r.top[k]);
+            r.l[k] = quad_sum(r.l[k]);
+        }
+        const float m = row_value(r.m), my_top = row_value(r.top), my_l = row_value(r.l);
         if (!cx.warp_wait(L::kOFull, seg & 1)) return;
         fence_after();
-        // The segment's partial.  With one tile of rows both warpgroups hold half of the tokens:
-        // each gets the other's state (through S, idle now) and adds half of the columns.
         float y[4] = {0.f, kNegInf, 0.f, 0.f};
         if (!two) {
-            tmem_st4(s, r.m, r.top, r.l, 0.f);
+            tmem_st4(s, m, my_top, my_l, 0.f);
             wait_st();
             fence_before();
             mbar_arrive(cx.bar(L::kXch));
@@ -666,51 +715,53 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             wait_ld(y);
         }
         const bool mine = two || n > b, theirs = !two && n > (b ^ 1);   // who had a tile
-        const float top = fmaxf(r.top, y[1]);   // a warpgroup without one has -inf
+        const float top = fmaxf(my_top, y[1]);   // a warpgroup without one has -inf
         // raw units for the join; what the rounding of the maximum moves goes into the weights
         const float M = top == kNegInf ? kNegInf : top / c2, at = top == kNegInf ? 0.f : M * c2;
         const float lo = top == kNegInf ? 0.f : fmaf(M, c2, -at);
-        const float w_mine = ex2(r.m - at - lo), w_theirs = theirs ? ex2(y[0] - at - lo) : 0.f;
-        const float sum = (mine ? r.l * w_mine : 0.f) + (theirs ? y[2] * w_theirs : 0.f);
-        const int slot = cta + w.unit0 + w.m, rt = two ? b : 0;
-        const int rows = min(a.per_tile, w.r.nb - w.first_branch() - rt * a.per_tile) * d.G;
-        const bool live = row < rows && slot < a.slots;
-        if (b == 0 && row == 0) {   // the unit's slots, from its first and its last segment
-            int2* us = a.unit_slots + (size_t)w.row * a.row_units + w.m;
-            if (i0 == 0) us->x = slot;
-            if (w.i_end == w.T) us->y = slot;
+        const float w_mine = ex2(m - at - lo), w_theirs = theirs ? ex2(y[0] - at - lo) : 0.f;
+        const float sum = (mine ? my_l * w_mine : 0.f) + (theirs ? y[2] * w_theirs : 0.f);
+        const int rt = two ? b : 0;
+        const bool live = row < (rt ? w.rows1 : w.rows0) && w.slot < a.slots;
+        const size_t at_slot = (size_t)w.slot * a.row_tiles + rt;
+        if (live && (two || b == 0)) {
+            a.part_ml[at_slot * kRows + row] = make_float2(M, sum);
+            // the branch's slots, from its unit's first and last segment
+            const int j = row / d.G;
+            int4* to = a.join + (size_t)(w.branch + rt * a.per_tile + j) * d.hkv + w.row % d.hkv;
+            if (row == j * d.G) {
+                if (w.flags & kSegFirst) {
+                    to->x = w.slot;
+                    to->z = rt * kRows + row;
+                }
+                if (w.flags & kSegLast) to->y = w.slot;
+            }
         }
-        const size_t at_slot = (size_t)slot * a.row_tiles + rt;
-        if (live && (two || b == 0)) a.part_ml[at_slot * kRows + row] = make_float2(M, sum);
         float4* out = a.part_o + at_slot * (D / 4) * kRows + row;
         const int c_begin = two ? 0 : b * (D / 2), c_end = two ? D : c_begin + D / 2;
 #pragma unroll 1
-        for (int c = c_begin; c < c_end; c += 32) {
-            float u[32], v[32];
-            if (mine) {
-                tmem_ld32(o + c, u);
-                wait_ld(u);
-            }
+        for (int c = c_begin; c < c_end; c += 16) {
+            float u[16], v[16];
+            tmem_ld16(o + c, u);   // (a warpgroup without a tile reads what it does not use)
+            tmem_ld16(lane + tmem_o<D>(b ^ 1) + c, v);
+            wait_ld(u, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = mine ? u[i] * w_mine : 0.f;
-            if (theirs) {
-                tmem_ld32(lane + tmem_o<D>(b ^ 1) + c, v);
-                wait_ld(v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = fmaf(v[i], w_theirs, u[i]);
+            for (int i = 0; i < 16; ++i) {
+                u[i] = mine ? u[i] * w_mine : 0.f;
+                if (theirs) u[i] = fmaf(v[i], w_theirs, u[i]);
             }
             if (live) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
+                for (int i = 0; i < 16; i += 4)
                     __stcg(out + (size_t)((c + i) / 4) * kRows, make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]));
             }
         }
         fence_before();
         mbar_arrive(cx.bar(L::kEpi));
-        ++seg;
     }
 }
 
+// ------------------------------------------------------------------ scheduler (one warp)
 // Inclusive scan of (x, y) over a warp.
 __device__ __forceinline__ int2 warp_scan(int2 v) {
 #pragma unroll
@@ -724,23 +775,43 @@ __device__ __forceinline__ int2 warp_scan(int2 v) {
     return v;
 }
 
-// This CTA's run, up to 32 rows: every warp for itself, a lane a row.
-__device__ __forceinline__ Sched schedule_warp(const AttnArgs& a) {
-    const int lane = threadIdx.x & 31;
+// This CTA's run.  Lane l owns rows [l per, (l + 1) per): a scan of their places gives the
+// list's length and, with it, the lane and then the row that hold the run's first place.
+__device__ __forceinline__ Sched find_run(const AttnArgs& a) {
+    const int lane = threadIdx.x & 31, R = a.p.d.R;
+    const int per = (R + 31) / 32, r0 = min(R, lane * per), r1 = min(R, r0 + per);
+    int2 x = make_int2(0, 0);
     RowInfo i{};
-    if (lane < a.p.d.R) i = row_info(a, lane);
-    const int n = i.mt * unit_len(i);
-    const int2 s = warp_scan(make_int2(n, i.mt));
-    const int V = __shfl_sync(kFull, s.x, 31), at = s.x - n;
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
+        i = row_info(a, r);
+        x.x += i.mt * unit_len(i);
+        x.y += i.mt;
+    }
+    const int2 s = warp_scan(x);
+    const int V = __shfl_sync(kFull, s.x, 31);
+    int at = s.x - x.x, units = s.y - x.y;
     Sched out{};
     const Runs runs(V, gridDim.x, a.div_ctas);
     if ((int)blockIdx.x >= runs.P) return out;
-    out.v = runs.begin(blockIdx.x);
-    out.v_end = runs.begin(blockIdx.x + 1);
-    const int src = __ffs(__ballot_sync(kFull, out.v >= at && out.v < at + n)) - 1;
-    out.row = src;
+    const int v = runs.begin(blockIdx.x), v_end = runs.begin(blockIdx.x + 1);
+    const bool here = v >= at && v < at + x.x;
+    const int src = __ffs(__ballot_sync(kFull, here)) - 1;
+    int row = r0;
+    if (here && per > 1) {
+        for (;; ++row) {
+            i = row_info(a, row);
+            const int n = i.mt * unit_len(i);
+            if (v < at + n) break;
+            at += n;
+            units += i.mt;
+        }
+    }
+    out.v = v;
+    out.v_end = v_end;
+    out.row = __shfl_sync(kFull, row, src);
     out.base = __shfl_sync(kFull, at, src);
-    out.units = __shfl_sync(kFull, s.y - i.mt, src);
+    out.units = __shfl_sync(kFull, units, src);
     out.r.n16 = __shfl_sync(kFull, i.n16, src);
     out.r.n8 = __shfl_sync(kFull, i.n8, src);
     out.r.T16 = (out.r.n16 + kTok - 1) / kTok;
@@ -751,46 +822,90 @@ __device__ __forceinline__ Sched schedule_warp(const AttnArgs& a) {
     return out;
 }
 
-// The same for any number: a block scan over the rows (threads own contiguous ones), then the
-// thread whose rows hold the run's first place hands over where that is.
+// Publishes the run's segments, and an end.
 template <int D>
-__device__ __noinline__ void schedule_block(const AttnArgs& a, char* smem) {
+__device__ void walk(const AttnArgs& a, const Ctx& cx, char* smem, Sched s) {
     using L = Smem<D>;
-    Sched* out = reinterpret_cast<Sched*>(smem + L::kSched);
-    int2* sums = reinterpret_cast<int2*>(smem + L::kSums);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.p.d.R;
-    const int per = (R + kThreads - 1) / kThreads, r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    int2 x = make_int2(0, 0);
-    for (int r = r0; r < r1; ++r) {
-        const RowInfo i = row_info(a, r);
-        x.x += i.mt * unit_len(i);
-        x.y += i.mt;
+    const int G = a.p.d.G, per_unit = a.row_tiles * a.per_tile;
+    int seg = 0, m = 0;
+    RowInfo r = s.r;
+    int T = r.T16 + r.T8;
+    if (r.mt > 1) {
+        m = (s.v - s.base) / (T + kSegCost);
+        s.base += m * (T + kSegCost);
     }
-    const int2 s = warp_scan(x);
-    if (lane == 31) sums[warp] = s;
-    if (tid == 0) *out = Sched{};
-    __syncthreads();
-    int V = 0, at = s.x - x.x, units = s.y - x.y;
-    for (int i = 0; i < kWarps; ++i) {
-        const int2 z = sums[i];
-        V += z.x;
-        if (i < warp) {
-            at += z.x;
-            units += z.y;
+    auto publish = [&](const Seg& x) {
+        const int z = seg % L::kSegs;
+        if (seg >= L::kSegs && !cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1)) return false;
+        *reinterpret_cast<Seg*>(smem + L::kSeg + z * 64) = x;
+        mbar_arrive(cx.bar(L::kSegFull + z));
+        ++seg;
+        return true;
+    };
+    while (s.v < s.v_end) {
+        while (s.v >= s.base + T + kSegCost) {   // the unit that holds place v
+            s.base += T + kSegCost;
+            if (++m >= r.mt) {
+                do {
+                    s.units += r.mt;
+                    if (++s.row >= a.p.d.R) {
+                        s.v = s.v_end;   // (counts that changed during the call)
+                        break;
+                    }
+                    r = row_info(a, s.row);
+                    T = r.T16 + r.T8;
+                } while (T == 0 || r.mt == 0);
+                m = 0;
+            }
+        }
+        if (s.v >= s.v_end) break;
+        Seg x;
+        x.i = max(s.v - s.base - kSegCost, 0);
+        x.i_end = min(s.v_end - s.base - kSegCost, T);
+        s.v = min(s.base + kSegCost + T, s.v_end);
+        if (x.i >= x.i_end) continue;
+        x.f8 = T < 65536 ? (int)((unsigned)x.i * r.T8 / (unsigned)T) : (int)((long long)x.i * r.T8 / T);
+        x.err = (int)((long long)x.i * r.T8 - (long long)x.f8 * T);
+        x.row = s.row;
+        x.n16 = r.n16;
+        x.n8 = r.n8;
+        x.T = T;
+        x.T8 = r.T8;
+        const int b0 = m * per_unit, left = r.nb - b0;
+        x.branch = r.b0 + b0;
+        x.rows0 = min(left, a.per_tile) * G;
+        x.rows1 = max(min(left - a.per_tile, a.per_tile), 0) * G;
+        x.slot = blockIdx.x + s.units + m;
+        x.flags = (x.i == 0 ? kSegFirst : 0) | (x.i_end == T ? kSegLast : 0) |
+                  (a.row_tiles > 1 && left > a.per_tile ? kSegTwo : 0);
+        if (!publish(x)) return;
+    }
+    Seg end{};
+    end.flags = kSegEnd;
+    publish(end);
+}
+
+// Tells the join which branches have no prefix token (a CTA's share of the branches).
+__device__ void no_prefix(const AttnArgs& a) {
+    const LayerDims& d = a.p.d;
+    for (int b = blockIdx.x * 32 + (threadIdx.x & 31); b < a.p.branches; b += gridDim.x * 32) {
+        int pre = 0;
+        bool has = true;
+        if (a.p.branch_start) {   // the last prefix that starts at or before b
+            int hi = d.batch;
+            while (hi - pre > 1) {
+                const int mid = (pre + hi) / 2;
+                if (__ldg(a.p.branch_start + mid) <= b) pre = mid;
+                else hi = mid;
+            }
+            has = __ldg(a.p.branch_start + pre) <= b && b < __ldg(a.p.branch_start + pre + 1);
+        }
+        for (int g = 0; g < d.hkv; ++g) {
+            const int row = pre * d.hkv + g;
+            if (!has || (__ldg(a.p.c.n_bf16 + row) <= 0 && __ldg(a.p.c.n_fp8 + row) <= 0))
+                a.join[(size_t)b * d.hkv + g] = make_int4(0, -1, 0, 0);
         }
     }
-    const Runs runs(V, gridDim.x, a.div_ctas);
-    if ((int)blockIdx.x < runs.P) {
-        const int v0 = runs.begin(blockIdx.x);
-        for (int r = r0; r < r1 && at <= v0; ++r) {
-            const RowInfo i = row_info(a, r);
-            const int n = i.mt * unit_len(i);
-            if (v0 < at + n) *out = Sched{v0, runs.begin(blockIdx.x + 1), at, r, units, i};
-            at += n;
-            units += i.mt;
-        }
-    }
-    __syncthreads();
 }
 
 template <int D, int FMT>
@@ -813,8 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         const int i = tid;
         int n = 1;
         if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 2) ||
-            (i >= L::kScFull && i < L::kScFull + 2) || i >= L::kCvt)
+            (i >= L::kScFull && i < L::kScFull + 2) || i == L::kCvt || i == L::kCvt + 1)
             n = 128;
+        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 18;   // the producer, the products, 16 warps
         if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + 2)) n = 256;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -825,8 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
         prefetch_map(&a.tm_v8);
     }
-    // (a prefetch reads nothing that the kernel uses)
-    if (warp == 0) {
+    if (warp == 3) {   // (a prefetch reads nothing that the kernel uses)
         const int r = min(lane, a.p.d.R - 1);
         prefetch_l2(a.p.c.n_bf16 + r);
         prefetch_l2(a.p.c.n_fp8 + r);
@@ -836,39 +951,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
-    if (!a.p.early_start) pdl_wait();
-    Sched sched;
-    if (a.p.d.R <= 32) {
-        sched = schedule_warp(a);
-    } else {
-        schedule_block<D>(a, smem);
-        sched = *reinterpret_cast<const Sched*>(smem + L::kSched);
-    }
-    if (sched.v < sched.v_end) {   // the same for the whole CTA
-        // registers go to the softmax warpgroups: 80 + 2 x 72 + 2 x 128 = the 5 x 96 at launch
-        if (warp < 4) set_regs<80, false>();
-        if (warp == 0) {
-            if (lane == 0) produce<D>(a, cx, base, Walk(a, sched));
+    // Registers go to the softmax warpgroups: 80 + 2 x 72 + 2 x 128 = the 5 x 96 at launch.  Bounded
+    // waits start when the previous kernel has finished.
+    if (warp < 4) {
+        set_regs<80, false>();
+        if (warp == 3) {
+            if (!a.p.early_start) pdl_wait();
+            const Sched sched = find_run(a);
+            if (lane == 0) walk<D>(a, cx, smem, sched);
+            __syncwarp();
+            pdl_wait();   // the workspace is the previous call's until it has finished
+            no_prefix(a);
+        } else if (warp == 0) {
+            if (lane == 0) {
+                if (!a.p.early_start) pdl_wait();
+                produce<D>(a, cx, smem, base);
+            }
         } else if (warp == 1) {
             if (lane == 0) {
-                pdl_wait();   // bounded waits start when the previous kernel has finished
-                multiply<D>(a, cx, base, tmem, Walk(a, sched));
+                pdl_wait();
+                multiply<D>(cx, smem, base, tmem);
             }
-        } else if (warp >= 16) {
-            set_regs<72, false>();
-            pdl_wait();
-            convert<D, FMT, 1>(a, cx, smem, tid - 512, Walk(a, sched));
-        } else if (warp >= 12) {
-            set_regs<72, false>();
-            pdl_wait();
-            convert<D, FMT, 0>(a, cx, smem, tid - 384, Walk(a, sched));
-        } else if (warp >= 4) {
-            set_regs<128, true>();
-            pdl_wait();
-            softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2, Walk(a, sched), blockIdx.x);
         }
+    } else if (warp < 12) {
+        set_regs<128, true>();
+        pdl_wait();
+        softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2);
+    } else {
+        set_regs<72, false>();
+        pdl_wait();
+        convert<D, FMT>(a, cx, smem, tid & 127, (warp - 12) >> 2);
     }
-    if (blockIdx.x == 0 && warp == 3) pdl_wait();   // the grid outlasts the previous kernel even with nothing to do
     __syncwarp();
     fence_before();
     __syncthreads();
@@ -879,67 +992,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ join
-// One block per (branch, key head): thread = (4 dimensions, query of the group).  The partials
-// of the row in CTA order and the own part, joined in float32; o is rounded to bf16.  The
-// loads of a batch of partials are all in flight at once.
+// One block per (branch, key head): thread = (4 dimensions, query of the group), four times:
+// each quarter of the block takes every fourth partial, its loads all in flight at once; the
+// quarters and the own part are joined in float32 in a fixed order, and o rounded to bf16.
+// Differences of two maxima are small where a weight counts, so float32 keeps them.
 template <int D>
-__global__ void __launch_bounds__(D) prefix_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kBatch = 10;
+__global__ void __launch_bounds__(4 * D) prefix_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kBatch = 5;
+    __shared__ float2 sm_ml[4][4];
+    __shared__ float4 sm_o[4][D];
     const LayerDims& d = a.p.d;
-    const int jq = threadIdx.x & 3, c4 = threadIdx.x >> 2;
+    const int tid = threadIdx.x % D, part = threadIdx.x / D, jq = tid & 3, c4 = tid >> 2;
     const int b = divided(blockIdx.x, a.div_hkv), g = blockIdx.x - b * d.hkv;
+    const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
+    const size_t mi = (size_t)blockIdx.x * 4 + jq, at = (((size_t)b * d.hq + g * d.G + jq) * D) / 4 + c4;
     pdl_launch_dependents();
     pdl_wait();
-    if (jq >= d.G) return;
-    const size_t mi = (size_t)blockIdx.x * 4 + jq, at = (((size_t)b * d.hq + g * d.G + jq) * D) / 4 + c4;
-    float2 own = make_float2(kNegInf, 0.f);
+    const int4 info = __ldcg(a.join + blockIdx.x);
+    float M = kNegInf, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.p.ml_own) {
-        own = a.p.ml_own[mi];
-        acc = reinterpret_cast<const float4*>(a.p.o_own)[at];
-    }
-    int pre = 0, b0 = 0;
-    bool has = true;
-    if (a.p.branch_start) {   // the last prefix that starts at or before b
-        int hi = d.batch;
-        while (hi - pre > 1) {
-            const int mid = (pre + hi) / 2;
-            if (__ldg(a.p.branch_start + mid) <= b) pre = mid;
-            else hi = mid;
+    if (part == 0 && a.p.ml_own && jq < d.G) {
+        const float2 own = a.p.ml_own[mi];
+        const float4 o = reinterpret_cast<const float4*>(a.p.o_own)[at];
+        if (own.y != 0.f) {   // L = 0: no own tokens
+            M = own.x;
+            L = own.y;
+            acc = make_float4(L * o.x, L * o.y, L * o.z, L * o.w);
         }
-        b0 = __ldg(a.p.branch_start + pre);
-        has = b0 <= b && b < __ldg(a.p.branch_start + pre + 1);
-        b0 = max(b0, 0);
     }
-    const int row = pre * d.hkv + g, m = divided(b - b0, a.div_unit);
-    const int in_unit = b - b0 - m * a.row_tiles * a.per_tile, rt = in_unit >= a.per_tile;
-    const int rr = (in_unit - rt * a.per_tile) * d.G + jq;
-    int2 slots = make_int2(0, -1);
-    if (has) {
-        slots = __ldcg(a.unit_slots + (size_t)row * a.row_units + min(m, a.row_units - 1));
-        if (min(__ldg(a.p.c.n_bf16 + row), d.cap_o) <= 0 && min(__ldg(a.p.c.n_fp8 + row), d.cap_q) <= 0) slots.y = -1;
-        slots.x = max(slots.x, 0);
-        slots.y = min(slots.y, a.slots - 1);
-    }
-    const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    float M = own.y != 0.f ? own.x : kNegInf, L = own.y;   // L = 0: no own tokens
-    acc = own.y != 0.f ? make_float4(L * acc.x, L * acc.y, L * acc.z, L * acc.w) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = slots.x; c <= slots.y; c += kBatch) {
+    const int last = jq < d.G ? min(info.y, a.slots - 1) : -1;
+    for (int c = max(info.x, 0) + part; c <= last; c += 4 * kBatch) {
         float2 ml[kBatch];
         float4 x[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             ml[q] = make_float2(kNegInf, 0.f);
-            if (c + q <= slots.y) {
-                const size_t s = (size_t)(c + q) * a.row_tiles + rt;
-                ml[q] = __ldcg(a.part_ml + s * kRows + rr);
-                x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + rr);
+            if (c + 4 * q <= last) {
+                const size_t s = (size_t)(c + 4 * q) * a.row_tiles + info.z / kRows;
+                ml[q] = __ldcg(a.part_ml + s * kRows + info.z % kRows + jq);
+                x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + info.z % kRows + jq);
             }
         }
         float mb = M;
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, ml[q].y != 0.f ? ml[q].x : kNegInf);
-        // differences are small where a weight counts, so float32 keeps them
         const float f = M == mb ? 1.f : ex2((M - mb) * c2);
         M = mb;
         L *= f;
@@ -952,6 +1048,24 @@ __global__ void __launch_bounds__(D) prefix_join_kernel(const __grid_constant__ 
             acc.x = fmaf(x[q].x, w, acc.x); acc.y = fmaf(x[q].y, w, acc.y);
             acc.z = fmaf(x[q].z, w, acc.z); acc.w = fmaf(x[q].w, w, acc.w);
         }
+    }
+    sm_o[part][tid] = acc;
+    if (c4 == 0) sm_ml[part][jq] = make_float2(M, L);
+    __syncthreads();
+    if (part != 0 || jq >= d.G) return;
+#pragma unroll
+    for (int q = 1; q < 4; ++q) M = fmaxf(M, sm_ml[q][jq].y != 0.f ? sm_ml[q][jq].x : kNegInf);
+    L = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float2 ml = sm_ml[q][jq];
+        if (ml.y == 0.f) continue;
+        const float w = ml.x == M ? 1.f : ex2((ml.x - M) * c2);
+        const float4 x = sm_o[q][tid];
+        L = fmaf(ml.y, w, L);
+        acc.x = fmaf(x.x, w, acc.x); acc.y = fmaf(x.y, w, acc.y);
+        acc.z = fmaf(x.z, w, acc.z); acc.w = fmaf(x.w, w, acc.w);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     reinterpret_cast<uint2*>(a.p.o)[at] =
@@ -1000,9 +1114,9 @@ bool make_q_map(CUtensorMap* m, const void* base, const LayerDims& d, int branch
 }
 
 struct PrefixWs {
-    size_t part_o, part_ml, unit_slots, total;
+    size_t part_o, part_ml, join, total;
     long long slots, units, places;
-    int per_tile, row_tiles, row_units;
+    int per_tile, row_tiles;
 };
 
 // A segment's partial goes to slot (CTA + unit): along the list each next segment raises one
@@ -1012,14 +1126,13 @@ PrefixWs ws_layout(const LayerDims& d, int branches) {
     PrefixWs w{};
     w.per_tile = kRows / d.G;
     w.row_tiles = branches > w.per_tile ? 2 : 1;
-    w.row_units = (branches + w.row_tiles * w.per_tile - 1) / (w.row_tiles * w.per_tile);
     w.units = (long long)d.hkv * (d.batch + branches / (w.row_tiles * w.per_tile));
     w.places = w.units * (((long long)d.cap_o + kTok - 1) / kTok + ((long long)d.cap_q + kTok - 1) / kTok + kSegCost);
     w.slots = kMaxCtas + w.units;
     auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
     const size_t rows = (size_t)w.slots * w.row_tiles * kRows;
     size_t off = 0;
-    w.unit_slots = off; off = al(off + sizeof(int2) * (size_t)d.R * w.row_units);
+    w.join = off;    off = al(off + sizeof(int4) * (size_t)branches * d.hkv);
     w.part_ml = off; off = al(off + sizeof(float2) * rows);
     w.part_o = off;  off = al(off + sizeof(float) * rows * d.D);
     w.total = off;
@@ -1043,8 +1156,7 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     a.slots = (int)w.slots;
     a.per_tile = w.per_tile;
     a.row_tiles = w.row_tiles;
-    a.unit_slots = reinterpret_cast<int2*>((char*)ws + w.unit_slots);
-    a.row_units = w.row_units;
+    a.join = reinterpret_cast<int4*>((char*)ws + w.join);
     a.part_ml = reinterpret_cast<float2*>((char*)ws + w.part_ml);
     a.part_o = reinterpret_cast<float4*>((char*)ws + w.part_o);
     const long long r16 = (long long)d.R * d.cap_o, r8 = (long long)d.R * d.cap_q;
@@ -1081,7 +1193,7 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
         lc.dynamicSmemBytes = (size_t)bytes;
         if ((err = cudaLaunchKernelEx(&lc, kernel, a)) != cudaSuccess) return err;
         lc.gridDim = dim3((unsigned)blocks);
-        lc.blockDim = dim3((unsigned)d.D);
+        lc.blockDim = dim3(4 * (unsigned)d.D);
         lc.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&lc, join, a);
     };
