@@ -15,9 +15,8 @@
 // that the run that holds them has that many tiles less.
 // prefix_join_kernel joins the partials and the branch's own part.
 //
-// A CTA: warp 3 walks the run and hands its segments to the others through shared memory,
-// warp 0 streams K and V by TMA through a ring of slots (a slot is a tile's K or its V),
-// warp 1 issues the products, two warpgroups do the softmax, each with its own S, P and O
+// A CTA: warp 0 walks the run, streams K and V by TMA through a ring of slots (a slot is a
+// tile's K or its V) and hands the segments to the others through shared memory, warp 1 issues the products, two warpgroups do the softmax, each with its own S, P and O
 // in tensor memory and its own state, so that neither waits for the other, and two
 // warpgroups rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits), one K,
 // one V.  With one tile of rows the softmax
@@ -25,9 +24,11 @@
 // segment; with two each has its rows, and a token tile is loaded and converted once for
 // both.  Either way a softmax job is one S, and the jobs alternate.
 // P takes the place of S.  The K scale of an FP8 token enters the exponent's factor, its V
-// scale is folded into P.  The softmax reference m moves only when a logit exceeds it by
-// 2^8, so O is seldom rescaled.  P is rounded to bf16 once, the rounding that o itself
-// gets; the sum is of the unrounded values.
+// scale is folded into P.
+// S is read once: the softmax reference m is the maximum of a segment's first columns and
+// moves only when a logit exceeds it by 2^32 (float32 and bf16 have the range), so O is
+// hardly ever rescaled.  P is rounded to bf16 once, the rounding that o itself gets; the
+// sum is of the unrounded values.
 // The loops over a tile's columns are not unrolled past 16: a short call runs each piece of
 // code once or twice, and fetching it cost more than the arithmetic.
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
@@ -270,78 +271,6 @@ __device__ __forceinline__ void fp8x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
-// ------------------------------------------------------------------ producer (one thread)
-template <int D>
-__device__ void produce(const AttnArgs& a, const Ctx& cx, const char* gsmem, uint32_t smem) {
-    using L = Smem<D>;
-    const LayerDims& d = a.p.d;
-    int e = 0, seg = 0;
-    uint32_t ph[3] = {0, 0, 0}, last[3] = {0, 0, 0};   // by barrier (full, raw K, raw V): parity of each slot's next
-                                                       // phase, the slots whose last load it has
-    bool ok = true, waited = !a.p.early_start;
-    Seg w{};
-    auto load = [&](const Tile& x, bool v) {
-        const int s = e % L::kSlots;
-        if (e >= L::kSlots && !cx.wait(L::kEmptyB + s, ((e / L::kSlots) & 1) ^ 1)) return false;
-        const bool conv = x.fp8 || (v && x.valid < kTok);
-        const int kind = conv ? (v ? 2 : 1) : 0;
-        const uint32_t dst = smem + L::kRing + s * L::kSlot;
-        const uint32_t bar = cx.bar((kind == 0 ? L::kFullB : kind == 1 ? L::kRawB : L::kRawB + L::kSlots) + s);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            if (i == kind) ph[i] ^= 1u << s;
-            last[i] = i == kind ? last[i] | (1u << s) : last[i] & ~(1u << s);
-        }
-        if (x.fp8) {
-            mbar_expect_tx(bar, kTok * D);
-            tma_load_2d(dst + L::kRaw, v ? &a.tm_v8 : &a.tm_k8, 0, w.row * d.cap_q + x.idx * kTok, bar);
-        } else {
-            mbar_expect_tx(bar, L::kSlot);
-            const int y = w.row * d.cap_o + x.idx * kTok;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * L::kRegion, v ? &a.tm_v16 : &a.tm_k16, 64 * c, y, bar);
-        }
-        ++e;
-        return true;
-    };
-    while (ok && thread_segment<D>(cx, gsmem, seg, w)) {
-        Tiles tiles(w);
-        // The segment's queries follow its first tiles: an early-started call fills its whole
-        // ring before the wait for the previous kernel, and a later segment's queries wait
-        // until the products of the one before have read theirs, which its first tile need not.
-        const int n = w.i_end - w.i, ahead = min(n, seg == 0 && a.p.early_start ? L::kSlots / 2 : 1);
-        for (int j = 0; ok && j < n; ++j) {
-            const Tile x = tiles.next();
-            ok = load(x, false) && load(x, true);
-            if (!ok || j != ahead - 1) continue;
-            if (!waited) {
-                pdl_wait();
-                waited = true;
-            }
-            if (seg > 0 && !(ok = cx.wait(L::kQEmpty, (seg - 1) & 1))) continue;
-            const int count = w.flags & kSegTwo ? 2 : 1;
-            mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
-            for (int t = 0; t < count; ++t)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem + L::kQ + t * L::kQTile + c * L::kRegion, &a.tm_q, 64 * c, 0, w.row % d.hkv,
-                                w.branch + t * a.per_tile, cx.bar(L::kQFull));
-            ++seg;
-        }
-    }
-    // copies in flight land before the CTA ends, also when it gives up
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        for (int s = 0; s < L::kSlots; ++s)
-            if ((last[i] >> s) & 1u)
-                for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar((i == 0 ? L::kFullB : i == 1 ? L::kRawB : L::kRawB + L::kSlots) + s),
-                                                                 ((ph[i] >> s) & 1u) ^ 1u); ++z) {
-                }
-    if (seg > 0)
-        for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kQFull), (seg - 1) & 1); ++z) {
-        }
-}
-
 // ------------------------------------------------------------------ products (one thread)
 // Softmax job x of a segment belongs to warpgroup x & 1: token tile x with one tile of
 // rows, token tile x / 2 with two.  S of job x + 1 is issued before P V of job x, and so
@@ -512,30 +441,30 @@ struct Rows {
     float m[4], top[4], l[4];
 };
 
-// 16 columns of S from column s on, times their K scales (FP8); columns from `valid` on are
-// no tokens.  v[k][2 g + e]: row k, column 8 g + 2 (t % 4) + e.
+// 32 columns of S from column s on, times their K scales (FP8); columns from `valid` on are
+// no tokens.  v[k][g]: row k, columns 8 g + 2 (t % 4) and the next.
 template <bool FP8>
-__device__ __forceinline__ void logits16(uint32_t s, int valid, const float* sk, float2 (&v)[4][2]) {
-    float2 k[2];
+__device__ __forceinline__ void logits32(uint32_t s, int valid, const float* sk, float2 (&v)[4][4]) {
     const int col = 2 * (threadIdx.x & 3);
+    float a[16], b[16];
+    tmem_ld_16x256b_x4(s, a);
+    tmem_ld_16x256b_x4(s + (16u << 16), b);
+    float2 k[4];
     if (FP8) {
-        k[0] = *reinterpret_cast<const float2*>(sk + col);
-        k[1] = *reinterpret_cast<const float2*>(sk + 8 + col);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) k[g] = *reinterpret_cast<const float2*>(sk + 8 * g + col);
     }
-    float a[8], b[8];
-    tmem_ld_16x256b_x2(s, a);
-    tmem_ld_16x256b_x2(s + (16u << 16), b);
     wait_ld(a, b);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < 4; ++g) {
         v[0][g] = make_float2(a[4 * g], a[4 * g + 1]);
         v[1][g] = make_float2(a[4 * g + 2], a[4 * g + 3]);
         v[2][g] = make_float2(b[4 * g], b[4 * g + 1]);
         v[3][g] = make_float2(b[4 * g + 2], b[4 * g + 3]);
     }
-    if (valid < 16) {
+    if (valid < 32) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 if (8 * g + col >= valid) v[r][g].x = kNegInf;
@@ -544,7 +473,7 @@ __device__ __forceinline__ void logits16(uint32_t s, int valid, const float* sk,
     }
     if (FP8) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r][g] = mul2(v[r][g], k[g]);
     }
@@ -567,85 +496,97 @@ __device__ __forceinline__ float row_value(const float (&x)[4]) {
     return lane < 16 ? (lane < 8 ? y0 : y1) : (lane < 24 ? y2 : y3);
 }
 
-// One job: S at column s of the warp's lanes becomes P.  O (column o) is idle while it
-// lasts: the product into S came after the last one into O.  S is read twice, 16 columns at
-// a time.
+// The reference of some of the warp's rows moves at column c of a job: by a whole number of
+// log2 units, so that what was weighed with the old one -- O and the job's first c columns of
+// P (column s) -- is rescaled exactly, by ff for the row of this lane.
+template <int D>
+__device__ __noinline__ void rescale(uint32_t s, uint32_t o, int c, float ff) {
+    wait_st();
+#pragma unroll 1
+    for (int i = 0; i < D; i += 16) {
+        float x[16];
+        tmem_ld16(o + i, x);
+        wait_ld(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= ff;
+        tmem_st16(o + i, x);
+    }
+#pragma unroll 1
+    for (int i = 0; i < c / 2; i += 16) {   // two to a column
+        float x[16];
+        tmem_ld16(s + i, x);
+        wait_ld(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t w = __float_as_uint(x[e]);
+            x[e] = __uint_as_float(pack_bf16(bf16_lo(w) * ff, bf16_hi(w) * ff));
+        }
+        tmem_st16(s + i, x);
+    }
+    wait_st();
+}
+
+// One job: S at column s of the warp's lanes becomes P, 32 columns at a time.  O (column o)
+// is idle while it lasts: the product into S came after the last one into O.
 template <int D, bool FP8>
 __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
                                             const float* sv, float c2, Rows& r) {
-    float2 v[4][2];
-    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+    const float2 cc = make_float2(c2, c2);
 #pragma unroll 1
-    for (int c = 0; c < kTok; c += 16) {
-        logits16<FP8>(s + c, valid - c, sk + c, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            mx[k] = fmaxf(fmaxf(fmaxf(mx[k], v[k][0].x), fmaxf(v[k][0].y, v[k][1].x)), v[k][1].y);
-    }
-    bool move = first;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (!FP8) mx[k] *= c2;
-        r.top[k] = fmaxf(r.top[k], mx[k]);
-        move |= mx[k] > r.m[k] + 8.f;
-    }
-    if (__any_sync(kFull, move)) {
-        float f[4];
+    for (int c = 0; c < kTok; c += 32) {
+        float2 v[4][4];
+        logits32<FP8>(s + c, valid - c, sk + c, v);
+        float mx[4];
+        bool move = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float top = quad_max(mx[k]);
-            f[k] = 1.f;
-            if (first) {
-                r.m[k] = top == kNegInf ? 0.f : top;
-            } else if (top > r.m[k] + 8.f) {
-                f[k] = ex2(r.m[k] - top);
+            const float m0 = fmaxf(fmaxf(v[k][0].x, v[k][0].y), fmaxf(v[k][1].x, v[k][1].y));
+            const float m1 = fmaxf(fmaxf(v[k][2].x, v[k][2].y), fmaxf(v[k][3].x, v[k][3].y));
+            mx[k] = FP8 ? fmaxf(m0, m1) : fmaxf(m0, m1) * c2;
+            r.top[k] = fmaxf(r.top[k], mx[k]);
+            move |= mx[k] > r.m[k] + 32.f;
+        }
+        if (first) {   // (column 0 is always a token)
+            first = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float t = quad_max(mx[k]);
+                r.m[k] = t == kNegInf ? 0.f : t;
+            }
+        } else if (__any_sync(kFull, move)) {
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float up = fmaxf(ceilf(quad_max(mx[k]) - r.m[k]), 0.f);
+                f[k] = ex2(-up);
+                r.m[k] += up;
                 r.l[k] *= f[k];
-                r.m[k] = top;
             }
+            rescale<D>(s, o, c, row_value(f));
         }
-        if (!first) {
-            const float ff = row_value(f);
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                float x[16];
-                tmem_ld16(o + c, x);
-                wait_ld(x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= ff;
-                tmem_st16(o + c, x);
-            }
-        }
-    }
-    const float2 cc = make_float2(c2, c2);
-    float2 l[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) l[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int c = 0; c < kTok; c += 16) {
-        logits16<FP8>(s + c, valid - c, sk + c, v);
-        float2 f[2];
+        float2 f[4];
         if (FP8) {
-            f[0] = *reinterpret_cast<const float2*>(sv + c + 2 * (threadIdx.x & 3));
-            f[1] = *reinterpret_cast<const float2*>(sv + c + 8 + 2 * (threadIdx.x & 3));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) f[g] = *reinterpret_cast<const float2*>(sv + c + 8 * g + 2 * (threadIdx.x & 3));
         }
-        uint32_t lo[4], hi[4];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
+        uint32_t lo[8], hi[8];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 m2 = make_float2(-r.m[k], -r.m[k]);
+            float2 l = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < 4; ++g) {
                 float2 p = FP8 ? add2(v[k][g], m2) : fma2(v[k][g], cc, m2);
                 p = make_float2(ex2(p.x), ex2(p.y));
-                l[k] = add2(l[k], p);
+                l = add2(l, p);
                 if (FP8) p = mul2(p, f[g]);
                 (k < 2 ? lo : hi)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
             }
+            r.l[k] += l.x + l.y;
         }
-        tmem_st_16x128b_x2(s + c / 2, lo);   // over columns of S that have been read
-        tmem_st_16x128b_x2(s + c / 2 + (16u << 16), hi);
+        tmem_st_16x128b_x4(s + c / 2, lo);   // over columns of S that have been read
+        tmem_st_16x128b_x4(s + c / 2 + (16u << 16), hi);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r.l[k] += l[k].x + l[k].y;
     wait_st();
 }
 
@@ -761,7 +702,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     }
 }
 
-// ------------------------------------------------------------------ scheduler (one warp)
+// ------------------------------------------------------------------ scheduler and producer (one warp)
 // Inclusive scan of (x, y) over a warp.
 __device__ __forceinline__ int2 warp_scan(int2 v) {
 #pragma unroll
@@ -822,67 +763,138 @@ __device__ __forceinline__ Sched find_run(const AttnArgs& a) {
     return out;
 }
 
-// Publishes the run's segments, and an end.
+// Walks the run (one thread): loads every segment's tiles and queries, and publishes the
+// segment once its first loads are on their way (the other roles need it, and their code,
+// only when those land).
 template <int D>
-__device__ void walk(const AttnArgs& a, const Ctx& cx, char* smem, Sched s) {
+__device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t smem, Sched s) {
     using L = Smem<D>;
-    const int G = a.p.d.G, per_unit = a.row_tiles * a.per_tile;
-    int seg = 0, m = 0;
+    const LayerDims& d = a.p.d;
+    const int per_unit = a.row_tiles * a.per_tile;
+    int seg = 0, e = 0, m = 0;              // segments and entries so far; place of the unit in its row
+    uint32_t ph[3] = {0, 0, 0}, last[3] = {0, 0, 0};   // by barrier (full, raw K, raw V): parity of each slot's next
+                                                       // phase, the slots whose last load it has
     RowInfo r = s.r;
     int T = r.T16 + r.T8;
     if (r.mt > 1) {
         m = (s.v - s.base) / (T + kSegCost);
         s.base += m * (T + kSegCost);
     }
-    auto publish = [&](const Seg& x) {
-        const int z = seg % L::kSegs;
-        if (seg >= L::kSegs && !cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1)) return false;
-        *reinterpret_cast<Seg*>(smem + L::kSeg + z * 64) = x;
-        mbar_arrive(cx.bar(L::kSegFull + z));
-        ++seg;
+    Seg x{};
+    auto load = [&](const Tile& t, bool v) {
+        const int z = e % L::kSlots;
+        if (e >= L::kSlots && !cx.wait(L::kEmptyB + z, ((e / L::kSlots) & 1) ^ 1)) return false;
+        const int kind = t.fp8 || (v && t.valid < kTok) ? (v ? 2 : 1) : 0;
+        const uint32_t dst = smem + L::kRing + z * L::kSlot;
+        const uint32_t bar = cx.bar((kind == 0 ? L::kFullB : kind == 1 ? L::kRawB : L::kRawB + L::kSlots) + z);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            if (i == kind) ph[i] ^= 1u << z;
+            last[i] = i == kind ? last[i] | (1u << z) : last[i] & ~(1u << z);
+        }
+        if (t.fp8) {
+            mbar_expect_tx(bar, kTok * D);
+            tma_load_2d(dst + L::kRaw, v ? &a.tm_v8 : &a.tm_k8, 0, x.row * d.cap_q + t.idx * kTok, bar);
+        } else {
+            mbar_expect_tx(bar, L::kSlot);
+            const int y = x.row * d.cap_o + t.idx * kTok;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * L::kRegion, v ? &a.tm_v16 : &a.tm_k16, 64 * c, y, bar);
+        }
+        ++e;
         return true;
     };
-    while (s.v < s.v_end) {
-        while (s.v >= s.base + T + kSegCost) {   // the unit that holds place v
-            s.base += T + kSegCost;
-            if (++m >= r.mt) {
-                do {
-                    s.units += r.mt;
-                    if (++s.row >= a.p.d.R) {
-                        s.v = s.v_end;   // (counts that changed during the call)
-                        break;
-                    }
-                    r = row_info(a, s.row);
-                    T = r.T16 + r.T8;
-                } while (T == 0 || r.mt == 0);
-                m = 0;
+    bool ok = true, waited = !a.p.early_start;
+    for (;;) {
+        // the next segment
+        bool any = false;
+        while (ok && !any && s.v < s.v_end) {
+            while (s.v >= s.base + T + kSegCost) {   // the unit that holds place v
+                s.base += T + kSegCost;
+                if (++m >= r.mt) {
+                    do {
+                        s.units += r.mt;
+                        if (++s.row >= d.R) {
+                            s.v = s.v_end;   // (counts that changed during the call)
+                            break;
+                        }
+                        r = row_info(a, s.row);
+                        T = r.T16 + r.T8;
+                    } while (T == 0 || r.mt == 0);
+                    m = 0;
+                }
+                if (s.v >= s.v_end) break;
             }
+            if (s.v >= s.v_end) break;
+            x.i = max(s.v - s.base - kSegCost, 0);
+            x.i_end = min(s.v_end - s.base - kSegCost, T);
+            s.v = min(s.base + kSegCost + T, s.v_end);
+            any = x.i < x.i_end;
         }
-        if (s.v >= s.v_end) break;
-        Seg x;
-        x.i = max(s.v - s.base - kSegCost, 0);
-        x.i_end = min(s.v_end - s.base - kSegCost, T);
-        s.v = min(s.base + kSegCost + T, s.v_end);
-        if (x.i >= x.i_end) continue;
-        x.f8 = T < 65536 ? (int)((unsigned)x.i * r.T8 / (unsigned)T) : (int)((long long)x.i * r.T8 / T);
+        const int z = seg % L::kSegs;
+        Seg* out = reinterpret_cast<Seg*>(gsmem + L::kSeg + z * 64);
+        if (!any) {
+            if (!ok || (seg >= L::kSegs && !cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) break;
+            out->flags = kSegEnd;
+            mbar_arrive(cx.bar(L::kSegFull + z));
+            break;
+        }
+        x.f8 = x.i == 0 ? 0 : T < 65536 ? (int)((unsigned)x.i * r.T8 / (unsigned)T) : (int)((long long)x.i * r.T8 / T);
         x.err = (int)((long long)x.i * r.T8 - (long long)x.f8 * T);
         x.row = s.row;
         x.n16 = r.n16;
         x.n8 = r.n8;
         x.T = T;
         x.T8 = r.T8;
-        const int b0 = m * per_unit, left = r.nb - b0;
-        x.branch = r.b0 + b0;
-        x.rows0 = min(left, a.per_tile) * G;
-        x.rows1 = max(min(left - a.per_tile, a.per_tile), 0) * G;
-        x.slot = blockIdx.x + s.units + m;
+        const int left = r.nb - m * per_unit;
+        x.branch = r.b0 + m * per_unit;
         x.flags = (x.i == 0 ? kSegFirst : 0) | (x.i_end == T ? kSegLast : 0) |
                   (a.row_tiles > 1 && left > a.per_tile ? kSegTwo : 0);
-        if (!publish(x)) return;
+        // The segment's queries follow its first tiles: an early-started call fills its whole
+        // ring before the wait for the previous kernel, and a later segment's queries wait
+        // until the products of the one before have read theirs, which its first tile need not.
+        Tiles tiles(x);
+        const int n = x.i_end - x.i, ahead = min(n, seg == 0 && a.p.early_start ? L::kSlots / 2 : 1);
+#pragma unroll 1
+        for (int j = 0; ok && j < n; ++j) {
+            const Tile t = tiles.next();
+            ok = load(t, false) && load(t, true);
+            if (!ok || j != ahead - 1) continue;
+            if (!waited) {
+                pdl_wait();
+                waited = true;
+            }
+            if (seg > 0 && !(ok = cx.wait(L::kQEmpty, (seg - 1) & 1))) continue;
+            const int count = x.flags & kSegTwo ? 2 : 1;
+            mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
+#pragma unroll 1
+            for (int q = 0; q < count; ++q)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(smem + L::kQ + q * L::kQTile + c * L::kRegion, &a.tm_q, 64 * c, 0,
+                                x.row - divided(x.row, a.div_hkv) * d.hkv, x.branch + q * a.per_tile, cx.bar(L::kQFull));
+            if (seg >= L::kSegs && !(ok = cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) continue;
+            x.rows0 = min(left, a.per_tile) * d.G;
+            x.rows1 = max(min(left - a.per_tile, a.per_tile), 0) * d.G;
+            x.slot = blockIdx.x + s.units + m;
+            *out = x;
+            mbar_arrive(cx.bar(L::kSegFull + z));
+            ++seg;
+        }
     }
-    Seg end{};
-    end.flags = kSegEnd;
-    publish(end);
+    if (!waited) pdl_wait();
+    // copies in flight land before the CTA ends, also when it gives up
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll 1
+        for (int z = 0; z < L::kSlots; ++z)
+            if ((last[i] >> z) & 1u)
+                for (int k = 0; k < kSpinLimit && !mbar_try_wait(cx.bar((i == 0 ? L::kFullB : i == 1 ? L::kRawB : L::kRawB + L::kSlots) + z),
+                                                                 ((ph[i] >> z) & 1u) ^ 1u); ++k) {
+                }
+    if (seg > 0)
+        for (int k = 0; k < kSpinLimit && !mbar_try_wait(cx.bar(L::kQFull), (seg - 1) & 1); ++k) {
+        }
 }
 
 // Tells the join which branches have no prefix token (a CTA's share of the branches).
@@ -930,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 2) ||
             (i >= L::kScFull && i < L::kScFull + 2) || i == L::kCvt || i == L::kCvt + 1)
             n = 128;
-        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 18;   // the producer, the products, 16 warps
+        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 17;   // the products, 16 warps
         if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + 2)) n = 256;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -941,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
         prefetch_map(&a.tm_v8);
     }
-    if (warp == 3) {   // (a prefetch reads nothing that the kernel uses)
+    if (warp == 0) {   // (a prefetch reads nothing that the kernel uses)
         const int r = min(lane, a.p.d.R - 1);
         prefetch_l2(a.p.c.n_bf16 + r);
         prefetch_l2(a.p.c.n_fp8 + r);
@@ -955,18 +967,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     // waits start when the previous kernel has finished.
     if (warp < 4) {
         set_regs<80, false>();
-        if (warp == 3) {
+        if (warp == 0) {
             if (!a.p.early_start) pdl_wait();
             const Sched sched = find_run(a);
-            if (lane == 0) walk<D>(a, cx, smem, sched);
-            __syncwarp();
+            if (lane == 0) produce<D>(a, cx, smem, base, sched);
+        } else if (warp == 3) {
             pdl_wait();   // the workspace is the previous call's until it has finished
             no_prefix(a);
-        } else if (warp == 0) {
-            if (lane == 0) {
-                if (!a.p.early_start) pdl_wait();
-                produce<D>(a, cx, smem, base);
-            }
         } else if (warp == 1) {
             if (lane == 0) {
                 pdl_wait();
