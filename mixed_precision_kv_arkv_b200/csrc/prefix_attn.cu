@@ -4,9 +4,9 @@
 // The queries of a prefix's branches that meet the same key head are the rows of one
 // matrix (row = branch x query of the group, tiles of 128 rows), so the prefix is read
 // once for all of them and both products run on the tensor cores:
-//   S[128 rows][128 tokens] = Q K^T,   O[128 rows][D] += P V,   P = 2^(S c - m).
+//   S[128 rows][64 tokens] = Q K^T,   O[128 rows][D] += P V,   P = 2^(S c - m).
 //
-// Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 128 tokens
+// Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 64 tokens
 // are the bf16 and the FP8 tiles of the prefix row, interleaved evenly, because an FP8
 // tile has twice the arithmetic per byte.  The tiles of all units form one list, cut into
 // equal runs, one a CTA and one CTA an SM; a run that crosses units is several segments,
@@ -51,11 +51,11 @@ using namespace tc;
 constexpr float kNegInf = -INFINITY;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 128;            // query rows of a tile
-constexpr int kTok = 128;             // tokens of a tile
+constexpr int kTok = 64;              // tokens of a tile
 constexpr int kWarps = 20;            // 4 of single roles, 2 x 4 softmax, 2 x 4 conversion
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;         // of one call
-constexpr int kSegCost = 3;           // a segment's start and end, in tiles
+constexpr int kSegCost = 5;           // a segment's start and end, in tiles
 constexpr int kSpinLimit = 1 << 20;   // polls of one wait
 
 struct RowInfo {
@@ -81,7 +81,7 @@ struct Seg {
 // ------------------------------------------------------------------ shared memory
 template <int D>
 struct Smem {
-    static constexpr int kSlots = 5;
+    static constexpr int kSlots = 10;                       // five tiles
     static constexpr int kSegs = 2;                         // segments on their way from the scheduler
     static constexpr int kSlot = kTok * D * 2;              // a K or V tile in bf16
     static constexpr int kRegion = kTok * 128;              // 64 dimensions of it (128-byte rows, swizzled)
@@ -89,28 +89,28 @@ struct Smem {
     static constexpr int kQ = 0;                            // two tiles of queries
     static constexpr int kQTile = kRows * D * 2;
     static constexpr int kRing = 2 * kQTile;
-    static constexpr int kScale = kRing + kSlots * kSlot;   // float [2][2][kTok]: K (log2 units) and V scales
-    static constexpr int kBars = kScale + 2 * 2 * kTok * 4;
+    static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K (log2 units) and V scales
+    static constexpr int kScales = 4;
+    static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
     // mbarriers.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
     // the tile has to be converted first (kConvB tells when): each barrier then has one
     // reader that sees every one of its phases, whichever kinds of tile come in between.
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
-                         kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 2, kScFull = kPFull + 2,
-                         kScFree = kScFull + 2, kOFull = kScFree + 2, kXch = kOFull + 1, kEpi = kXch + 1,
+                         kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4, kPvDone = kPFull + 4,
+                         kScFull = kPvDone + 2, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
                          kFin = kEpi + 1, kCvt = kFin + 1, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
                          kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
     static constexpr int kSeg = kMisc + 16;                             // Seg [kSegs]
-    static constexpr int kSums = kSeg + kSegs * 64;                     // int2 [32]: scan of the rows
-    static constexpr int kBytes = kSums + 32 * 8;
+    static constexpr int kBytes = kSeg + kSegs * 64;
     static_assert(sizeof(Seg) <= 64 && kBytes <= 232448, "shared memory of one CTA");
 };
 
-// tensor-memory columns: S (and P) of the two warpgroups, then their O
+// tensor-memory columns: two S (and P) of each of the two softmax warpgroups, then their O
 constexpr uint32_t kTmemCols = 512;
-__host__ __device__ constexpr uint32_t tmem_s(int b) { return (uint32_t)b * kTok; }
+__host__ __device__ constexpr uint32_t tmem_s(int wg, int buf) { return (uint32_t)(2 * wg + buf) * kTok; }
 template <int D>
-__host__ __device__ constexpr uint32_t tmem_o(int b) { return 2 * kTok + (uint32_t)b * D; }
+__host__ __device__ constexpr uint32_t tmem_o(int wg) { return 4 * kTok + (uint32_t)wg * D; }
 
 // ------------------------------------------------------------------ schedule
 struct AttnArgs {
@@ -178,8 +178,9 @@ struct Tile {
 // The tiles of a segment in order: after i tiles of a unit, floor(i T8 / T) are FP8.
 struct Tiles {
     int i, n16, n8, T, T8, f8, err;
-    __device__ __forceinline__ explicit Tiles(const Seg& s)
-        : i(s.i), n16(s.n16), n8(s.n8), T(s.T), T8(s.T8), f8(s.f8), err(s.err) {}
+    __device__ __forceinline__ explicit Tiles(const Seg& s)   // (a whole warp)
+        : i(uniform(s.i)), n16(uniform(s.n16)), n8(uniform(s.n8)), T(uniform(s.T)), T8(uniform(s.T8)), f8(uniform(s.f8)),
+          err(uniform(s.err)) {}
     __device__ __forceinline__ Tile next() {
         Tile x;
         err += T8;
@@ -218,17 +219,7 @@ struct Ctx {
     __device__ __forceinline__ bool warp_wait(int i, uint32_t parity) const { return __all_sync(kFull, wait(i, parity)); }
 };
 
-// Segment number `seg` from the scheduler (one thread); false at the end of the run.
-template <int D>
-__device__ __forceinline__ bool thread_segment(const Ctx& cx, const char* smem, int seg, Seg& out) {
-    using L = Smem<D>;
-    const int z = seg % L::kSegs;
-    if (!cx.wait(L::kSegFull + z, (seg / L::kSegs) & 1)) return false;
-    out = *reinterpret_cast<const Seg*>(smem + L::kSeg + z * 64);
-    mbar_arrive(cx.bar(L::kSegEmpty + z));
-    return !(out.flags & kSegEnd);
-}
-// The same for a warp.
+// Segment number `seg` from the scheduler, to a warp; false at the end of the run.
 template <int D>
 __device__ __forceinline__ bool warp_segment(const Ctx& cx, const char* smem, int seg, Seg& out) {
     using L = Smem<D>;
@@ -238,6 +229,17 @@ __device__ __forceinline__ bool warp_segment(const Ctx& cx, const char* smem, in
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bar(L::kSegEmpty + z));
     return !(out.flags & kSegEnd);
+}
+
+// Whether a phase is complete, at once.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -272,80 +274,112 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
 // ------------------------------------------------------------------ products (one thread)
-// Softmax job x of a segment belongs to warpgroup x & 1: token tile x with one tile of
-// rows, token tile x / 2 with two.  S of job x + 1 is issued before P V of job x, and so
-// after that of job x - 1, which read P from the same place.
+// Softmax job x of a segment belongs to warpgroup x & 1 and its S number (x >> 1) & 1: token
+// tile x with one tile of rows, token tile x / 2 with two.  S of job x may be issued once P V
+// of job x - 4, which read P from the same place, has been; whichever of the next S and the
+// next P V has its operands goes first.
+// (one warp, one lane of which issues)
 template <int D>
 __device__ void multiply(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false), kIdPV = idesc_bf16(kRows, D, true);
     int j = 0, seg = 0;            // tiles and segments so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
-    uint32_t p_ph = 0;             // parity of each warpgroup's next P
+    uint32_t p_ph = 0;             // parity of the next P of each of the four S
     bool ok = true;
+    const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
-    auto ready = [&](int e, bool converted) {   // entry e has landed (and been converted)
+    auto test = [&](int i, uint32_t parity) { return __all_sync(kFull, mbar_test(cx.bar(i), parity)) != 0; };
+    auto landed = [&](int e, bool converted) {   // entry e is there (and has been converted)
         const int s = e % L::kSlots;
         uint32_t& ph = converted ? conv : full;
-        const bool r = cx.wait((converted ? L::kConvB : L::kFullB) + s, (ph >> s) & 1u);
+        if (!test((converted ? L::kConvB : L::kFullB) + s, (ph >> s) & 1u)) return false;
         ph ^= 1u << s;
-        return r;
+        return true;
     };
-    Seg w;
-    while (ok && thread_segment<D>(cx, gsmem, seg, w)) {
+    Seg w{};
+    while (ok && warp_segment<D>(cx, gsmem, seg, w)) {
         Tiles tiles(w);
-        const bool two = w.flags & kSegTwo;
-        const int sh = two ? 1 : 0, n = w.i_end - w.i, jobs = n << sh;
-        ok = cx.wait(L::kQFull, seg & 1) && (seg == 0 || cx.wait(L::kEpi, (seg - 1) & 1));
-        uint32_t conv_v = 0;       // by job & 1: its V tile is converted
+        const bool two = uniform(w.flags) & kSegTwo;
+        const int sh = two ? 1 : 0, n = uniform(w.i_end) - tiles.i, jobs = n << sh;
+        ok = cx.warp_wait(L::kQFull, seg & 1) && (seg == 0 || cx.warp_wait(L::kEpi, (seg - 1) & 1));
+        uint32_t conv_v = 0;       // by job & 3: its V tile is converted
         Tile t{};
-        for (int x = 0; ok && x <= jobs; ++x) {
-            if (x < jobs) {        // S of job x
-                const int b = x & 1, e = 2 * (j + (x >> sh)), s = e % L::kSlots;
-                const bool opens = !two || b == 0, closes = !two || b == 1;   // the tile's first, last job
-                if (opens) {
-                    t = tiles.next();
-                    if (!(ok = ready(e, t.fp8))) break;
+        bool have = false, k_in = false, p_in = false, v_in = false;   // what is known of the next S, the next P V
+        int sx = 0, px = 0, idle = 0;
+#pragma unroll 1
+        while (ok && px < jobs) {
+            if (sx < jobs && sx < px + 4) {
+                const int b = sx & 1, e = 2 * (j + (sx >> sh)), s = e % L::kSlots;
+                if (two && b == 1) k_in = true;   // the tile that the job before has used
+                if (!k_in) {
+                    if (!have) t = tiles.next();
+                    have = true;
+                    k_in = landed(e, t.fp8);
+                }
+                if (k_in) {
                     fence_after();
-                }
-                conv_v = (conv_v & ~(1u << b)) | ((uint32_t)(t.fp8 || t.valid < kTok) << b);
-                const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
-                const uint64_t qd = q_desc + (uint64_t)(two ? b * (L::kQTile >> 4) : 0);
+                    conv_v = (conv_v & ~(1u << (sx & 3))) | ((uint32_t)(t.fp8 || t.valid < kTok) << (sx & 3));
+                    const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
+                    const uint64_t qd = q_desc + (uint64_t)(two ? b * (L::kQTile >> 4) : 0);
+                    const uint32_t to = tmem + tmem_s(b, (sx >> 1) & 1);
+                    if (leader) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2);
-                    mma_ss(tmem + tmem_s(b), qd + o, k_desc + o, kIdQK, k > 0);
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ss(to, qd + (uint64_t)((k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2),
+                                   k_desc + (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2), kIdQK, k > 0);
+                        commit(cx.bar(L::kSFull + (sx & 3)));
+                        if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
+                        if (sx + 1 == jobs) commit(cx.bar(L::kQEmpty));
+                    }
+                    __syncwarp();
+                    ++sx;
+                    have = k_in = false;
+                    idle = 0;
+                    continue;
                 }
-                commit(cx.bar(L::kSFull + b));
-                if (closes) commit(cx.bar(L::kEmptyB + s));
-                if (x + 1 == jobs) commit(cx.bar(L::kQEmpty));
             }
-            if (x > 0) {           // P V of job x - 1
-                const int y = x - 1, b = y & 1, e = 2 * (j + (y >> sh)) + 1, s = e % L::kSlots;
-                const bool opens = !two || b == 0, closes = !two || b == 1;
-                if (!(ok = cx.wait(L::kPFull + b, (p_ph >> b) & 1u) && (!opens || ready(e, (conv_v >> b) & 1u)))) break;
-                p_ph ^= 1u << b;
-                fence_after();
-                const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
-                const bool add = y >= 2;   // each warpgroup's first product of the segment starts its O
+            if (px < sx) {
+                const int b = px & 1, z = px & 3, e = 2 * (j + (px >> sh)) + 1, s = e % L::kSlots;
+                if (!p_in) p_in = test(L::kPFull + z, (p_ph >> z) & 1u);
+                if (p_in && !v_in) v_in = (two && b == 1) || landed(e, (conv_v >> z) & 1u);
+                if (p_in && v_in) {
+                    p_ph ^= 1u << z;
+                    fence_after();
+                    const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
+                    const bool add = px >= 2;   // each warpgroup's first product of the segment starts its O
+                    const uint32_t to = tmem + tmem_o<D>(b), from = tmem + tmem_s(b, (px >> 1) & 1);
+                    if (leader) {
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    mma_ts(tmem + tmem_o<D>(b), tmem + tmem_s(b) + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV,
-                           add || k > 0);
-                if (closes) commit(cx.bar(L::kEmptyB + s));
-                if (x == jobs) commit(cx.bar(L::kOFull));
+                        for (int k = 0; k < kTok / 16; ++k)
+                            mma_ts(to, from + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV, add || k > 0);
+                        commit(cx.bar(L::kPvDone + b));
+                        if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
+                        if (px + 1 == jobs) commit(cx.bar(L::kOFull));
+                    }
+                    __syncwarp();
+                    ++px;
+                    p_in = v_in = false;
+                    idle = 0;
+                    continue;
+                }
             }
+            if (++idle > 16 * kSpinLimit) {
+                *cx.abort_flag = 1;
+                atomicOr(cx.status, ARKV_STATUS_TIMEOUT);
+            }
+            if ((idle & 63) == 0 && __any_sync(kFull, *cx.abort_flag)) ok = false;
         }
         j += n;
         ++seg;
     }
     // every product has completed before tensor memory is freed
-    commit(cx.bar(L::kFin));
+    if (leader) commit(cx.bar(L::kFin));
     for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kFin), 0); ++z) {
     }
 }
 
-// ------------------------------------------------------------------ FP8 -> bf16 (128 threads, one a token)
+// ------------------------------------------------------------------ FP8 -> bf16 (128 threads, two a token)
 // kv = 0: the K tiles and the scales, 1: the V tiles, whose rows past the segment end
 // become zero in either format (stale bits must not meet P = 0).
 template <int D, int FMT>
@@ -354,22 +388,20 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, in
     const LayerDims& d = a.p.d;
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
     float* scales = reinterpret_cast<float*>(smem + L::kScale);
+    const int row = ct >> 1, h = ct & 1;   // token of the tile, half of its dimensions
+    const bool of_v = ct >= kTok;          // the scale that this thread loads: K of token ct, V of ct - 64
     int cvt = 0, f = 0, j = 0;   // uses of the read-before-write barrier (D = 64); FP8 tiles, tiles so far
     uint32_t raw_ph = 0;         // parity of each slot's next phase (of the K or V loads to convert)
     Seg w;
     for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
         Tiles tiles(w);
-        float sk = 1.f, sv = 0.f;   // of this thread's token in the segment's next FP8 tile
-        auto load_scales = [&](int idx) {
-            const int t = idx * kTok + ct;
-            sk = 1.f;               // past the end: a masked column
-            sv = 0.f;
-            if (kv == 0 && t < w.n8) {
-                sk = __ldg(a.p.c.sk + (size_t)w.row * d.cap_q + t) * c2;
-                sv = __ldg(a.p.c.sv + (size_t)w.row * d.cap_q + t);
-            }
+        float scale = 0.f;       // of the segment's next FP8 tile
+        auto load_scale = [&](int idx) {
+            const int t = idx * kTok + (ct & (kTok - 1));
+            scale = of_v ? 0.f : 1.f;   // past the end: a masked column
+            if (kv == 0 && t < w.n8) scale = __ldg((of_v ? a.p.c.sv : a.p.c.sk) + (size_t)w.row * d.cap_q + t) * (of_v ? 1.f : c2);
         };
-        load_scales(w.f8);
+        load_scale(w.f8);
 #pragma unroll 1
         for (const int end = w.i_end; tiles.i < end; ++j) {
             const Tile cur = tiles.next();
@@ -377,50 +409,52 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, in
             const bool tail = kv == 1 && !cur.fp8 && cur.valid < kTok;
             if (!cur.fp8 && !tail) continue;
             if (kv == 0) {
-                const int z = f & 1, use = f >> 1;
+                const int z = f % L::kScales, use = f / L::kScales;
                 if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // their last readers
-                scales[(2 * z) * kTok + ct] = sk;
-                scales[(2 * z + 1) * kTok + ct] = sv;
+                scales[2 * z * kTok + ct] = scale;
                 mbar_arrive(cx.bar(L::kScFull + z));
                 ++f;
-                load_scales(cur.idx + 1);   // the next ones, on their way during this tile
+                load_scale(cur.idx + 1);   // the next ones, on their way during this tile
             }
             if (!cx.warp_wait(L::kRawB + kv * L::kSlots + s, (raw_ph >> s) & 1u)) return;
             raw_ph ^= 1u << s;
             char* slot = smem + L::kRing + s * L::kSlot;
-            const bool zero = kv == 1 && ct >= cur.valid;
+            const bool zero = kv == 1 && row >= cur.valid;
             if (!tail) {
-                // 64 dimensions at a time, the upper half of a 128-byte row first: the codes lie
-                // where the lower half goes
-#pragma unroll 1
-                for (int h = D / 64 - 1; h >= 0; --h) {
-                    uint4 raw[4];
+                // D / 2 codes a thread.  A 128-byte row's codes lie where its lower half goes: both
+                // threads of the row (one warp) read before either writes; rows of 64 codes grow
+                // over other rows' codes, so all threads do.  The upper half goes through its
+                // 16-byte chunks in another order, which keeps the two halves' banks apart.
+                constexpr int N = D / 32;
+                uint4 raw[N];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        raw[c] = *reinterpret_cast<const uint4*>(
-                            slot + L::kRaw + (D == 128 ? sw128(ct, 4 * h + c) : sw64(ct, c)));
-                        if (zero) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if constexpr (D == 64) {   // rows grow over other threads' codes (D = 128: over their own alone)
-                        mbar_arrive(cx.bar(L::kCvt + kv));
-                        if (!cx.warp_wait(L::kCvt + kv, cvt++ & 1)) return;
-                    }
+                for (int c = 0; c < N; ++c) {
+                    const int at = D == 128 ? 4 * h + (c ^ (2 * h)) : 2 * h + c;
+                    raw[c] = *reinterpret_cast<const uint4*>(slot + L::kRaw + (D == 128 ? sw128(row, at) : sw64(row, at)));
+                    if (zero) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if constexpr (D == 64) {
+                    mbar_arrive(cx.bar(L::kCvt + kv));
+                    if (!cx.warp_wait(L::kCvt + kv, cvt++ & 1)) return;
+                } else {
+                    __syncwarp();
+                }
+                char* reg = slot + (D == 128 ? h * L::kRegion : 0);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint4 lo, hi;
-                        fp8x4_to_bf16<FMT>(raw[c].x, lo.x, lo.y);
-                        fp8x4_to_bf16<FMT>(raw[c].y, lo.z, lo.w);
-                        fp8x4_to_bf16<FMT>(raw[c].z, hi.x, hi.y);
-                        fp8x4_to_bf16<FMT>(raw[c].w, hi.z, hi.w);
-                        char* reg = slot + h * L::kRegion;
-                        *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * c)) = lo;
-                        *reinterpret_cast<uint4*>(reg + sw128(ct, 2 * c + 1)) = hi;
-                    }
+                for (int c = 0; c < N; ++c) {
+                    uint4 lo, hi;
+                    fp8x4_to_bf16<FMT>(raw[c].x, lo.x, lo.y);
+                    fp8x4_to_bf16<FMT>(raw[c].y, lo.z, lo.w);
+                    fp8x4_to_bf16<FMT>(raw[c].z, hi.x, hi.y);
+                    fp8x4_to_bf16<FMT>(raw[c].w, hi.z, hi.w);
+                    const int to = D == 128 ? 2 * (c ^ (2 * h)) : 4 * h + 2 * c;
+                    *reinterpret_cast<uint4*>(reg + sw128(row, to)) = lo;
+                    *reinterpret_cast<uint4*>(reg + sw128(row, to + 1)) = hi;
                 }
             } else if (zero) {
 #pragma unroll 1
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(slot + (c >> 3) * L::kRegion + ct * 128 + ((c & 7) << 4)) =
+                for (int c = h; c < D / 8; c += 2)
+                    *reinterpret_cast<uint4*>(slot + (c >> 3) * L::kRegion + row * 128 + ((c & 7) << 4)) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async();
@@ -526,11 +560,13 @@ __device__ __noinline__ void rescale(uint32_t s, uint32_t o, int c, float ff) {
     wait_st();
 }
 
-// One job: S at column s of the warp's lanes becomes P, 32 columns at a time.  O (column o)
-// is idle while it lasts: the product into S came after the last one into O.
+// One job: S at column s of the warp's lanes becomes P, 32 columns at a time.  first: the
+// warpgroup's first of the segment, whose O (column o) holds nothing yet; else O is idle when
+// the product of the job before has completed (a phase of `pv`).  False if that took too long.
 template <int D, bool FP8>
-__device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, int valid, const float* sk,
-                                            const float* sv, float c2, Rows& r) {
+__device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t pv_parity, uint32_t s, uint32_t o, bool first,
+                                            int valid, const float* sk, const float* sv, float c2, Rows& r) {
+    bool begin = first;
     const float2 cc = make_float2(c2, c2);
 #pragma unroll 1
     for (int c = 0; c < kTok; c += 32) {
@@ -546,8 +582,8 @@ __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, 
             r.top[k] = fmaxf(r.top[k], mx[k]);
             move |= mx[k] > r.m[k] + 32.f;
         }
-        if (first) {   // (column 0 is always a token)
-            first = false;
+        if (begin) {   // (column 0 is always a token)
+            begin = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float t = quad_max(mx[k]);
@@ -562,6 +598,8 @@ __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, 
                 r.m[k] += up;
                 r.l[k] *= f[k];
             }
+            if (!first && !cx.warp_wait(pv, pv_parity)) return false;
+            fence_after();
             rescale<D>(s, o, c, row_value(f));
         }
         float2 f[4];
@@ -588,6 +626,7 @@ __device__ __forceinline__ void softmax_job(uint32_t s, uint32_t o, bool first, 
         tmem_st_16x128b_x4(s + c / 2 + (16u << 16), hi);
     }
     wait_st();
+    return true;
 }
 
 template <int D>
@@ -595,10 +634,10 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     using L = Smem<D>;
     const LayerDims& d = a.p.d;
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
-    const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b), o = lane + tmem_o<D>(b);
+    const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b, 0), o = lane + tmem_o<D>(b);
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    int f = 0, xch = 0;        // FP8 tiles and exchanges so far
-    uint32_t s_ph = 0;         // parity of this warpgroup's next S
+    int f = 0, xch = 0, jobs = 0;   // FP8 tiles, exchanges and this warpgroup's jobs so far
+    uint32_t s_ph = 0;              // parity of the next of each of its two S
     Seg w;
     for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
         const bool two = w.flags & kSegTwo;
@@ -615,22 +654,29 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
 #pragma unroll 1
         for (int x = 0; x < n; ++x) {
             const Tile t = tiles.next();
-            const int z = f & 1, use = (f >> 1) & 1;
+            const int z = f % L::kScales, use = (f / L::kScales) & 1;
             f += t.fp8;
             if (!two && (x & 1) != b) continue;
-            if (!cx.warp_wait(L::kSFull + b, s_ph)) return;
-            s_ph ^= 1u;
+            const int buf = (two ? x : x >> 1) & 1;
+            if (!cx.warp_wait(L::kSFull + b + 2 * buf, (s_ph >> buf) & 1u)) return;
+            s_ph ^= 1u << buf;
             fence_after();
+            // of the product before: it is the barrier's current phase or the one before that,
+            // since this S came after the one before the last
+            const uint32_t pv_parity = (uint32_t)(jobs - 1) & 1u;
             if (t.fp8) {
                 if (!cx.warp_wait(L::kScFull + z, use)) return;   // complete: K came after the scales
                 const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
-                softmax_job<D, true>(s, o, first, t.valid, sk, sk + kTok, c2, r);
+                if (!softmax_job<D, true>(cx, L::kPvDone + b, pv_parity, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r))
+                    return;
             } else {
-                softmax_job<D, false>(s, o, first, t.valid, nullptr, nullptr, c2, r);
+                if (!softmax_job<D, false>(cx, L::kPvDone + b, pv_parity, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r))
+                    return;
             }
             first = false;
+            ++jobs;
             fence_before();
-            mbar_arrive(cx.bar(L::kPFull + b));
+            mbar_arrive(cx.bar(L::kPFull + b + 2 * buf));
             if (t.fp8) mbar_arrive_n(cx.bar(L::kScFree + z), two ? 1 : 2);   // 256 in all, whoever read them
         }
         // The segment's partial, a lane a row from here.  With one tile of rows both warpgroups
@@ -652,7 +698,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             mbar_arrive(cx.bar(L::kXch));
             if (!cx.warp_wait(L::kXch, xch++ & 1)) return;
             fence_after();
-            tmem_ld4(lane + tmem_s(b ^ 1), y);
+            tmem_ld4(lane + tmem_s(b ^ 1, 0), y);
             wait_ld(y);
         }
         const bool mine = two || n > b, theirs = !two && n > (b ^ 1);   // who had a tile
@@ -763,7 +809,7 @@ __device__ __forceinline__ Sched find_run(const AttnArgs& a) {
     return out;
 }
 
-// Walks the run (one thread): loads every segment's tiles and queries, and publishes the
+// Walks the run (one warp, one lane of which issues): loads every segment's tiles and queries, and publishes the
 // segment once its first loads are on their way (the other roles need it, and their code,
 // only when those land).
 template <int D>
@@ -781,9 +827,10 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
         s.base += m * (T + kSegCost);
     }
     Seg x{};
+    const bool leader = elect_one();
     auto load = [&](const Tile& t, bool v) {
         const int z = e % L::kSlots;
-        if (e >= L::kSlots && !cx.wait(L::kEmptyB + z, ((e / L::kSlots) & 1) ^ 1)) return false;
+        if (e >= L::kSlots && !cx.warp_wait(L::kEmptyB + z, ((e / L::kSlots) & 1) ^ 1)) return false;
         const int kind = t.fp8 || (v && t.valid < kTok) ? (v ? 2 : 1) : 0;
         const uint32_t dst = smem + L::kRing + z * L::kSlot;
         const uint32_t bar = cx.bar((kind == 0 ? L::kFullB : kind == 1 ? L::kRawB : L::kRawB + L::kSlots) + z);
@@ -792,15 +839,19 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
             if (i == kind) ph[i] ^= 1u << z;
             last[i] = i == kind ? last[i] | (1u << z) : last[i] & ~(1u << z);
         }
-        if (t.fp8) {
-            mbar_expect_tx(bar, kTok * D);
-            tma_load_2d(dst + L::kRaw, v ? &a.tm_v8 : &a.tm_k8, 0, x.row * d.cap_q + t.idx * kTok, bar);
-        } else {
-            mbar_expect_tx(bar, L::kSlot);
-            const int y = x.row * d.cap_o + t.idx * kTok;
+        const int y = x.row * (t.fp8 ? d.cap_q : d.cap_o) + t.idx * kTok;
+        if (leader) {
+            if (t.fp8) {
+                mbar_expect_tx(bar, kTok * D);
+                tma_load_2d(dst + L::kRaw, v ? &a.tm_v8 : &a.tm_k8, 0, y, bar);
+            } else {
+                mbar_expect_tx(bar, L::kSlot);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * L::kRegion, v ? &a.tm_v16 : &a.tm_k16, 64 * c, y, bar);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_2d(dst + c * L::kRegion, v ? &a.tm_v16 : &a.tm_k16, 64 * c, y, bar);
+            }
         }
+        __syncwarp();
         ++e;
         return true;
     };
@@ -834,9 +885,11 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
         const int z = seg % L::kSegs;
         Seg* out = reinterpret_cast<Seg*>(gsmem + L::kSeg + z * 64);
         if (!any) {
-            if (!ok || (seg >= L::kSegs && !cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) break;
-            out->flags = kSegEnd;
-            mbar_arrive(cx.bar(L::kSegFull + z));
+            if (!ok || (seg >= L::kSegs && !cx.warp_wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) break;
+            if (leader) {
+                out->flags = kSegEnd;
+                mbar_arrive(cx.bar(L::kSegFull + z));
+            }
             break;
         }
         x.f8 = x.i == 0 ? 0 : T < 65536 ? (int)((unsigned)x.i * r.T8 / (unsigned)T) : (int)((long long)x.i * r.T8 / T);
@@ -864,21 +917,27 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
                 pdl_wait();
                 waited = true;
             }
-            if (seg > 0 && !(ok = cx.wait(L::kQEmpty, (seg - 1) & 1))) continue;
-            const int count = x.flags & kSegTwo ? 2 : 1;
-            mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
+            if (seg > 0 && !(ok = cx.warp_wait(L::kQEmpty, (seg - 1) & 1))) continue;
+            const int count = x.flags & kSegTwo ? 2 : 1, head = x.row - divided(x.row, a.div_hkv) * d.hkv;
+            if (leader) {
+                mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
 #pragma unroll 1
-            for (int q = 0; q < count; ++q)
+                for (int q = 0; q < count; ++q)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(smem + L::kQ + q * L::kQTile + c * L::kRegion, &a.tm_q, 64 * c, 0,
-                                x.row - divided(x.row, a.div_hkv) * d.hkv, x.branch + q * a.per_tile, cx.bar(L::kQFull));
-            if (seg >= L::kSegs && !(ok = cx.wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) continue;
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(smem + L::kQ + q * L::kQTile + c * kRows * 128, &a.tm_q, 64 * c, 0, head,
+                                    x.branch + q * a.per_tile, cx.bar(L::kQFull));
+            }
+            __syncwarp();
+            if (seg >= L::kSegs && !(ok = cx.warp_wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) continue;
             x.rows0 = min(left, a.per_tile) * d.G;
             x.rows1 = max(min(left - a.per_tile, a.per_tile), 0) * d.G;
             x.slot = blockIdx.x + s.units + m;
-            *out = x;
-            mbar_arrive(cx.bar(L::kSegFull + z));
+            if (leader) {
+                *out = x;
+                mbar_arrive(cx.bar(L::kSegFull + z));
+            }
+            __syncwarp();
             ++seg;
         }
     }
@@ -939,11 +998,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     if (tid < L::kNumBars) {
         const int i = tid;
         int n = 1;
-        if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 2) ||
-            (i >= L::kScFull && i < L::kScFull + 2) || i == L::kCvt || i == L::kCvt + 1)
+        if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 4) ||
+            (i >= L::kScFull && i < L::kScFull + L::kScales) || i == L::kCvt || i == L::kCvt + 1)
             n = 128;
         if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 17;   // the products, 16 warps
-        if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + 2)) n = 256;
+        if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + L::kScales)) n = 256;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -970,15 +1029,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         if (warp == 0) {
             if (!a.p.early_start) pdl_wait();
             const Sched sched = find_run(a);
-            if (lane == 0) produce<D>(a, cx, smem, base, sched);
+            produce<D>(a, cx, smem, base, sched);
         } else if (warp == 3) {
             pdl_wait();   // the workspace is the previous call's until it has finished
             no_prefix(a);
         } else if (warp == 1) {
-            if (lane == 0) {
-                pdl_wait();
-                multiply<D>(cx, smem, base, tmem);
-            }
+            pdl_wait();
+            multiply<D>(cx, smem, base, uniform(tmem));
         }
     } else if (warp < 12) {
         set_regs<128, true>();

@@ -34,6 +34,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// One lane of a converged warp, always the same.  The single-thread instructions (products,
+// TMA) are issued under it from code that the whole warp runs: their operands are then
+// warp-uniform for the compiler; in code of one lane each took some 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+template <class T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // The registers a thread of this warpgroup may use from here on.
 template <int N, bool INC>
 __device__ __forceinline__ void set_regs() {
