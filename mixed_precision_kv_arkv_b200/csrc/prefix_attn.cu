@@ -16,8 +16,9 @@
 // prefix_join_kernel joins the partials and the branch's own part.
 //
 // A CTA: warp 0 walks the run, streams K and V by TMA through a ring of slots (a slot is a
-// tile's K or its V) and hands the segments to the others through shared memory, warp 1 issues the products, two warpgroups do the softmax, each with its own S, P and O
-// in tensor memory and its own state, so that neither waits for the other, and two
+// tile's K or its V) and hands the segments to the others through shared memory, warps
+// 1 and 2 issue the products, two warpgroups do the softmax, each with its own two S (and P)
+// and O in tensor memory and its own state, so that neither waits for the other, and two
 // warpgroups rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits), one K,
 // one V.  With one tile of rows the softmax
 // warpgroups take the token tiles in turn and their two O are added at the end of the
@@ -25,12 +26,10 @@
 // both.  Either way a softmax job is one S, and the jobs alternate.
 // P takes the place of S.  The K scale of an FP8 token enters the exponent's factor, its V
 // scale is folded into P.
-// S is read once: the softmax reference m is the maximum of a segment's first columns and
-// moves only when a logit exceeds it by 2^32 (float32 and bf16 have the range), so O is
-// hardly ever rescaled.  P is rounded to bf16 once, the rounding that o itself gets; the
+// The softmax reference m is the maximum of a segment's first tile and moves only when a
+// logit exceeds it by 2^32 (float32 and bf16 have the range), so O is hardly ever rescaled
+// and a job needs no maximum before its exponentials.  P is rounded to bf16 once, the rounding that o itself gets; the
 // sum is of the unrounded values.
-// The loops over a tile's columns are not unrolled past 16: a short call runs each piece of
-// code once or twice, and fetching it cost more than the arithmetic.
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
 // memory is freed and the call ends.
@@ -92,13 +91,13 @@ struct Smem {
     static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K (log2 units) and V scales
     static constexpr int kScales = 4;
     static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
-    // mbarriers.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
+    // mbarriers.  K is in the even slots, V in the odd ones.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
     // the tile has to be converted first (kConvB tells when): each barrier then has one
     // reader that sees every one of its phases, whichever kinds of tile come in between.
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
-                         kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4, kPvDone = kPFull + 4,
-                         kScFull = kPvDone + 2, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
-                         kFin = kEpi + 1, kCvt = kFin + 1, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
+                         kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4,
+                         kScFull = kPFull + 4, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
+                         kFin = kEpi + 1, kCvt = kFin + 2, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
                          kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
     static constexpr int kSeg = kMisc + 16;                             // Seg [kSegs]
@@ -231,17 +230,6 @@ __device__ __forceinline__ bool warp_segment(const Ctx& cx, const char* smem, in
     return !(out.flags & kSegEnd);
 }
 
-// Whether a phase is complete, at once.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -275,107 +263,104 @@ __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 6
 
 // ------------------------------------------------------------------ products (one thread)
 // Softmax job x of a segment belongs to warpgroup x & 1 and its S number (x >> 1) & 1: token
-// tile x with one tile of rows, token tile x / 2 with two.  S of job x may be issued once P V
-// of job x - 4, which read P from the same place, has been; whichever of the next S and the
-// next P V has its operands goes first.
-// (one warp, one lane of which issues)
+// tile x with one tile of rows, token tile x / 2 with two.  One warp issues the S, another the
+// P V (one lane each), so that neither product waits behind the other's operands; S of job x
+// follows the completion of P V of job x - 4, which read P from the same place.  (With one warp
+// for both, polling for whichever was ready, a tile of 64 took 0.5 us more: it shares its
+// scheduler with four busy warps, and its instructions were what a tile waited for.)
 template <int D>
-__device__ void multiply(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
+__device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D>;
-    constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false), kIdPV = idesc_bf16(kRows, D, true);
-    int j = 0, seg = 0;            // tiles and segments so far
+    constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false);
+    int j = 0;                     // tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
-    uint32_t p_ph = 0;             // parity of the next P of each of the four S
-    bool ok = true;
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
-    auto test = [&](int i, uint32_t parity) { return __all_sync(kFull, mbar_test(cx.bar(i), parity)) != 0; };
-    auto landed = [&](int e, bool converted) {   // entry e is there (and has been converted)
-        const int s = e % L::kSlots;
-        uint32_t& ph = converted ? conv : full;
-        if (!test((converted ? L::kConvB : L::kFullB) + s, (ph >> s) & 1u)) return false;
-        ph ^= 1u << s;
-        return true;
-    };
     Seg w{};
-    while (ok && warp_segment<D>(cx, gsmem, seg, w)) {
+    for (int seg = 0; warp_segment<D>(cx, gsmem, seg, w); ++seg) {
         Tiles tiles(w);
         const bool two = uniform(w.flags) & kSegTwo;
         const int sh = two ? 1 : 0, n = uniform(w.i_end) - tiles.i, jobs = n << sh;
-        ok = cx.warp_wait(L::kQFull, seg & 1) && (seg == 0 || cx.warp_wait(L::kEpi, (seg - 1) & 1));
-        uint32_t conv_v = 0;       // by job & 3: its V tile is converted
-        Tile t{};
-        bool have = false, k_in = false, p_in = false, v_in = false;   // what is known of the next S, the next P V
-        int sx = 0, px = 0, idle = 0;
+        if (!cx.warp_wait(L::kQFull, seg & 1) || (seg > 0 && !cx.warp_wait(L::kEpi, (seg - 1) & 1))) return;
 #pragma unroll 1
-        while (ok && px < jobs) {
-            if (sx < jobs && sx < px + 4) {
-                const int b = sx & 1, e = 2 * (j + (sx >> sh)), s = e % L::kSlots;
-                if (two && b == 1) k_in = true;   // the tile that the job before has used
-                if (!k_in) {
-                    if (!have) t = tiles.next();
-                    have = true;
-                    k_in = landed(e, t.fp8);
-                }
-                if (k_in) {
-                    fence_after();
-                    conv_v = (conv_v & ~(1u << (sx & 3))) | ((uint32_t)(t.fp8 || t.valid < kTok) << (sx & 3));
-                    const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
-                    const uint64_t qd = q_desc + (uint64_t)(two ? b * (L::kQTile >> 4) : 0);
-                    const uint32_t to = tmem + tmem_s(b, (sx >> 1) & 1);
-                    if (leader) {
+        for (int x = 0; x < jobs; ++x) {
+            const int b = x & 1, t = x >> sh, e = 2 * (j + t), s = e % L::kSlots;
+            if (!two || b == 0) {
+                const int before = t - (two ? 2 : 4);   // the tile whose P V frees this S
+                const int ev = 2 * (j + before) + 1;
+                if (before >= 0 && !cx.warp_wait(L::kEmptyB + ev % L::kSlots, (ev / L::kSlots) & 1)) return;
+                const bool c = tiles.next().fp8;
+                if (!cx.warp_wait((c ? L::kConvB : L::kFullB) + s, ((c ? conv : full) >> s) & 1u)) return;
+                if (c) conv ^= 1u << s;
+                else full ^= 1u << s;
+            }
+            fence_after();
+            const uint64_t k_desc = desc_sw128(smem + L::kRing + s * L::kSlot, 16, 1024);
+            const uint64_t qd = q_desc + (uint64_t)(two ? b * (L::kQTile >> 4) : 0);
+            const uint32_t to = tmem + tmem_s(b, (x >> 1) & 1);
+            if (leader) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_ss(to, qd + (uint64_t)((k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2),
-                                   k_desc + (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2), kIdQK, k > 0);
-                        commit(cx.bar(L::kSFull + (sx & 3)));
-                        if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
-                        if (sx + 1 == jobs) commit(cx.bar(L::kQEmpty));
-                    }
-                    __syncwarp();
-                    ++sx;
-                    have = k_in = false;
-                    idle = 0;
-                    continue;
-                }
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(to, qd + (uint64_t)((k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2),
+                           k_desc + (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2), kIdQK, k > 0);
+                commit(cx.bar(L::kSFull + (x & 3)));
+                if (x + 1 == jobs) commit(cx.bar(L::kQEmpty));
             }
-            if (px < sx) {
-                const int b = px & 1, z = px & 3, e = 2 * (j + (px >> sh)) + 1, s = e % L::kSlots;
-                if (!p_in) p_in = test(L::kPFull + z, (p_ph >> z) & 1u);
-                if (p_in && !v_in) v_in = (two && b == 1) || landed(e, (conv_v >> z) & 1u);
-                if (p_in && v_in) {
-                    p_ph ^= 1u << z;
-                    fence_after();
-                    const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
-                    const bool add = px >= 2;   // each warpgroup's first product of the segment starts its O
-                    const uint32_t to = tmem + tmem_o<D>(b), from = tmem + tmem_s(b, (px >> 1) & 1);
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
-                            mma_ts(to, from + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV, add || k > 0);
-                        commit(cx.bar(L::kPvDone + b));
-                        if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
-                        if (px + 1 == jobs) commit(cx.bar(L::kOFull));
-                    }
-                    __syncwarp();
-                    ++px;
-                    p_in = v_in = false;
-                    idle = 0;
-                    continue;
-                }
-            }
-            if (++idle > 16 * kSpinLimit) {
-                *cx.abort_flag = 1;
-                atomicOr(cx.status, ARKV_STATUS_TIMEOUT);
-            }
-            if ((idle & 63) == 0 && __any_sync(kFull, *cx.abort_flag)) ok = false;
+            __syncwarp();
         }
         j += n;
-        ++seg;
     }
-    // every product has completed before tensor memory is freed
-    if (leader) commit(cx.bar(L::kFin));
-    for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kFin), 0); ++z) {
+}
+
+template <int D>
+__device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
+    using L = Smem<D>;
+    constexpr uint32_t kIdPV = idesc_bf16(kRows, D, true);
+    int j = 0;                     // tiles so far
+    uint32_t full = 0, conv = 0;   // parity of each slot's next phase
+    uint32_t p_ph = 0;             // parity of the next P of each of the four S
+    const bool leader = elect_one();
+    Seg w{};
+    for (int seg = 0; warp_segment<D>(cx, gsmem, seg, w); ++seg) {
+        Tiles tiles(w);
+        const bool two = uniform(w.flags) & kSegTwo;
+        const int sh = two ? 1 : 0, n = uniform(w.i_end) - tiles.i, jobs = n << sh;
+#pragma unroll 1
+        for (int x = 0; x < jobs; ++x) {
+            const int b = x & 1, z = x & 3, e = 2 * (j + (x >> sh)) + 1, s = e % L::kSlots;
+            if (!two || b == 0) {
+                const Tile t = tiles.next();
+                const bool c = t.fp8 || t.valid < kTok;
+                if (!cx.warp_wait((c ? L::kConvB : L::kFullB) + s, ((c ? conv : full) >> s) & 1u)) return;
+                if (c) conv ^= 1u << s;
+                else full ^= 1u << s;
+            }
+            if (!cx.warp_wait(L::kPFull + z, (p_ph >> z) & 1u)) return;
+            p_ph ^= 1u << z;
+            fence_after();
+            const uint64_t v_desc = desc_sw128(smem + L::kRing + s * L::kSlot, L::kRegion, 1024);
+            const uint32_t to = tmem + tmem_o<D>(b), from = tmem + tmem_s(b, (x >> 1) & 1);
+            const bool add = x >= 2;   // each warpgroup's first product of the segment starts its O
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                    mma_ts(to, from + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV, add || k > 0);
+                if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
+                if (x + 1 == jobs) commit(cx.bar(L::kOFull));
+            }
+            __syncwarp();
+        }
+        j += n;
+    }
+}
+
+// Waits until every product of this warp has completed (before tensor memory is freed).
+template <int D>
+__device__ __forceinline__ void drain(const Ctx& cx, int which) {
+    using L = Smem<D>;
+    if (elect_one()) commit(cx.bar(L::kFin + which));
+    __syncwarp();
+    for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kFin + which), 0); ++z) {
     }
 }
 
@@ -390,18 +375,20 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, in
     float* scales = reinterpret_cast<float*>(smem + L::kScale);
     const int row = ct >> 1, h = ct & 1;   // token of the tile, half of its dimensions
     const bool of_v = ct >= kTok;          // the scale that this thread loads: K of token ct, V of ct - 64
+    constexpr int kAhead = 4;              // FP8 tiles between a scale's load and its use (a latency of HBM)
     int cvt = 0, f = 0, j = 0;   // uses of the read-before-write barrier (D = 64); FP8 tiles, tiles so far
     uint32_t raw_ph = 0;         // parity of each slot's next phase (of the K or V loads to convert)
     Seg w;
     for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
         Tiles tiles(w);
-        float scale = 0.f;       // of the segment's next FP8 tile
+        float scale[kAhead];     // of the segment's next FP8 tiles
         auto load_scale = [&](int idx) {
             const int t = idx * kTok + (ct & (kTok - 1));
-            scale = of_v ? 0.f : 1.f;   // past the end: a masked column
-            if (kv == 0 && t < w.n8) scale = __ldg((of_v ? a.p.c.sv : a.p.c.sk) + (size_t)w.row * d.cap_q + t) * (of_v ? 1.f : c2);
+            if (kv == 0 && t < w.n8) return __ldg((of_v ? a.p.c.sv : a.p.c.sk) + (size_t)w.row * d.cap_q + t);
+            return of_v ? 0.f : 1.f;   // past the end: a masked column
         };
-        load_scale(w.f8);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) scale[i] = load_scale(w.f8 + i);
 #pragma unroll 1
         for (const int end = w.i_end; tiles.i < end; ++j) {
             const Tile cur = tiles.next();
@@ -411,10 +398,12 @@ __device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, in
             if (kv == 0) {
                 const int z = f % L::kScales, use = f / L::kScales;
                 if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // their last readers
-                scales[2 * z * kTok + ct] = scale;
+                scales[2 * z * kTok + ct] = of_v ? scale[0] : scale[0] * c2;
                 mbar_arrive(cx.bar(L::kScFull + z));
                 ++f;
-                load_scale(cur.idx + 1);   // the next ones, on their way during this tile
+#pragma unroll
+                for (int i = 0; i + 1 < kAhead; ++i) scale[i] = scale[i + 1];
+                scale[kAhead - 1] = load_scale(cur.idx + kAhead);
             }
             if (!cx.warp_wait(L::kRawB + kv * L::kSlots + s, (raw_ph >> s) & 1u)) return;
             raw_ph ^= 1u << s;
@@ -475,44 +464,6 @@ struct Rows {
     float m[4], top[4], l[4];
 };
 
-// 32 columns of S from column s on, times their K scales (FP8); columns from `valid` on are
-// no tokens.  v[k][g]: row k, columns 8 g + 2 (t % 4) and the next.
-template <bool FP8>
-__device__ __forceinline__ void logits32(uint32_t s, int valid, const float* sk, float2 (&v)[4][4]) {
-    const int col = 2 * (threadIdx.x & 3);
-    float a[16], b[16];
-    tmem_ld_16x256b_x4(s, a);
-    tmem_ld_16x256b_x4(s + (16u << 16), b);
-    float2 k[4];
-    if (FP8) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) k[g] = *reinterpret_cast<const float2*>(sk + 8 * g + col);
-    }
-    wait_ld(a, b);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        v[0][g] = make_float2(a[4 * g], a[4 * g + 1]);
-        v[1][g] = make_float2(a[4 * g + 2], a[4 * g + 3]);
-        v[2][g] = make_float2(b[4 * g], b[4 * g + 1]);
-        v[3][g] = make_float2(b[4 * g + 2], b[4 * g + 3]);
-    }
-    if (valid < 32) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (8 * g + col >= valid) v[r][g].x = kNegInf;
-                if (8 * g + col + 1 >= valid) v[r][g].y = kNegInf;
-            }
-    }
-    if (FP8) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r][g] = mul2(v[r][g], k[g]);
-    }
-}
-
 // Over the four lanes of a row.
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
@@ -530,12 +481,10 @@ __device__ __forceinline__ float row_value(const float (&x)[4]) {
     return lane < 16 ? (lane < 8 ? y0 : y1) : (lane < 24 ? y2 : y3);
 }
 
-// The reference of some of the warp's rows moves at column c of a job: by a whole number of
-// log2 units, so that what was weighed with the old one -- O and the job's first c columns of
-// P (column s) -- is rescaled exactly, by ff for the row of this lane.
+// The reference of some of the warp's rows moves by a whole number of log2 units, so that O,
+// weighed with the old one, is rescaled exactly, by ff for the row of this lane.
 template <int D>
-__device__ __noinline__ void rescale(uint32_t s, uint32_t o, int c, float ff) {
-    wait_st();
+__device__ __noinline__ void rescale(uint32_t o, float ff) {
 #pragma unroll 1
     for (int i = 0; i < D; i += 16) {
         float x[16];
@@ -545,88 +494,95 @@ __device__ __noinline__ void rescale(uint32_t s, uint32_t o, int c, float ff) {
         for (int e = 0; e < 16; ++e) x[e] *= ff;
         tmem_st16(o + i, x);
     }
-#pragma unroll 1
-    for (int i = 0; i < c / 2; i += 16) {   // two to a column
-        float x[16];
-        tmem_ld16(s + i, x);
-        wait_ld(x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t w = __float_as_uint(x[e]);
-            x[e] = __uint_as_float(pack_bf16(bf16_lo(w) * ff, bf16_hi(w) * ff));
-        }
-        tmem_st16(s + i, x);
-    }
     wait_st();
 }
 
-// One job: S at column s of the warp's lanes becomes P, 32 columns at a time.  first: the
-// warpgroup's first of the segment, whose O (column o) holds nothing yet; else O is idle when
-// the product of the job before has completed (a phase of `pv`).  False if that took too long.
+// One job: S at column s of the warp's lanes becomes P.  The whole tile is one piece of code
+// (the exponentials set its pace, and everything else has to fit between them), which is run
+// again when the reference turns out too low -- rarely, and on the first job of a segment, when
+// there is none yet.  O (column o) then has to be idle: the product of the job before has
+// completed when it frees its V, entry pv.  False if that took too long.
 template <int D, bool FP8>
-__device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t pv_parity, uint32_t s, uint32_t o, bool first,
-                                            int valid, const float* sk, const float* sv, float c2, Rows& r) {
-    bool begin = first;
+__device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, uint32_t o, bool first, int valid,
+                                            const float* sk, const float* sv, float c2, Rows& r) {
     const float2 cc = make_float2(c2, c2);
-#pragma unroll 1
-    for (int c = 0; c < kTok; c += 32) {
-        float2 v[4][4];
-        logits32<FP8>(s + c, valid - c, sk + c, v);
+    const int col = 2 * (threadIdx.x & 3);
+    bool begin = first;
+    for (;;) {
+        // row k of the lane, columns 8 g + col and the next: va[4 g + 2 (k & 1) ..] (k < 2), vb
+        float va[32], vb[32];
+        tmem_ld_16x256b_x8(s, va);
+        tmem_ld_16x256b_x8(s + (16u << 16), vb);
+        wait_ld(va, vb);
+        if (valid < kTok) {   // columns that are no tokens
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (8 * (i / 4) + col + (i & 1) >= valid) va[i] = vb[i] = kNegInf;
+        }
         float mx[4];
-        bool move = false;
+        float2 l[4];
+        uint32_t pa[16], pb[16];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float m0 = fmaxf(fmaxf(v[k][0].x, v[k][0].y), fmaxf(v[k][1].x, v[k][1].y));
-            const float m1 = fmaxf(fmaxf(v[k][2].x, v[k][2].y), fmaxf(v[k][3].x, v[k][3].y));
-            mx[k] = FP8 ? fmaxf(m0, m1) : fmaxf(m0, m1) * c2;
+            mx[k] = kNegInf;
+            l[k] = make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            float2 ks = make_float2(1.f, 1.f), vs = make_float2(1.f, 1.f);
+            if (FP8) {
+                ks = *reinterpret_cast<const float2*>(sk + 8 * g + col);
+                vs = *reinterpret_cast<const float2*>(sv + 8 * g + col);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* v = (k < 2 ? va : vb) + 4 * g + 2 * (k & 1);
+                float2 x = make_float2(v[0], v[1]);
+                if (FP8) x = mul2(x, ks);
+                mx[k] = fmaxf(fmaxf(mx[k], x.x), x.y);
+                const float2 m2 = make_float2(-r.m[k], -r.m[k]);
+                float2 p = FP8 ? add2(x, m2) : fma2(x, cc, m2);
+                p = make_float2(ex2(p.x), ex2(p.y));
+                l[k] = add2(l[k], p);
+                if (FP8) p = mul2(p, vs);
+                (k < 2 ? pa : pb)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
+            }
+        }
+        bool move = begin;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (!FP8) mx[k] *= c2;
             r.top[k] = fmaxf(r.top[k], mx[k]);
             move |= mx[k] > r.m[k] + 32.f;
         }
-        if (begin) {   // (column 0 is always a token)
-            begin = false;
+        if (!__any_sync(kFull, move)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float t = quad_max(mx[k]);
+            for (int k = 0; k < 4; ++k) r.l[k] += l[k].x + l[k].y;
+            tmem_st_16x128b_x8(s, pa);   // over S, which has been read
+            tmem_st_16x128b_x8(s + (16u << 16), pb);
+            wait_st();
+            return true;
+        }
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float t = quad_max(mx[k]);
+            if (begin) {
                 r.m[k] = t == kNegInf ? 0.f : t;
-            }
-        } else if (__any_sync(kFull, move)) {
-            float f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float up = fmaxf(ceilf(quad_max(mx[k]) - r.m[k]), 0.f);
+            } else {
+                const float up = fmaxf(ceilf(t - r.m[k]), 0.f);
                 f[k] = ex2(-up);
                 r.m[k] += up;
                 r.l[k] *= f[k];
             }
-            if (!first && !cx.warp_wait(pv, pv_parity)) return false;
+        }
+        if (!begin) {
+            if (!cx.warp_wait(Smem<D>::kEmptyB + pv % Smem<D>::kSlots, (pv / Smem<D>::kSlots) & 1)) return false;
             fence_after();
-            rescale<D>(s, o, c, row_value(f));
+            rescale<D>(o, row_value(f));
         }
-        float2 f[4];
-        if (FP8) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) f[g] = *reinterpret_cast<const float2*>(sv + c + 8 * g + 2 * (threadIdx.x & 3));
-        }
-        uint32_t lo[8], hi[8];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 m2 = make_float2(-r.m[k], -r.m[k]);
-            float2 l = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float2 p = FP8 ? add2(v[k][g], m2) : fma2(v[k][g], cc, m2);
-                p = make_float2(ex2(p.x), ex2(p.y));
-                l = add2(l, p);
-                if (FP8) p = mul2(p, f[g]);
-                (k < 2 ? lo : hi)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
-            }
-            r.l[k] += l.x + l.y;
-        }
-        tmem_st_16x128b_x4(s + c / 2, lo);   // over columns of S that have been read
-        tmem_st_16x128b_x4(s + c / 2 + (16u << 16), hi);
+        begin = false;
     }
-    wait_st();
-    return true;
 }
 
 template <int D>
@@ -636,7 +592,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b, 0), o = lane + tmem_o<D>(b);
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    int f = 0, xch = 0, jobs = 0;   // FP8 tiles, exchanges and this warpgroup's jobs so far
+    int f = 0, xch = 0, j = 0;      // FP8 tiles, exchanges and tiles so far
     uint32_t s_ph = 0;              // parity of the next of each of its two S
     Seg w;
     for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
@@ -661,24 +617,21 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             if (!cx.warp_wait(L::kSFull + b + 2 * buf, (s_ph >> buf) & 1u)) return;
             s_ph ^= 1u << buf;
             fence_after();
-            // of the product before: it is the barrier's current phase or the one before that,
-            // since this S came after the one before the last
-            const uint32_t pv_parity = (uint32_t)(jobs - 1) & 1u;
+            if ((threadIdx.x & 127) == 0) mbar_arrive_n(cx.bar(L::kEmptyB + 2 * (j + x) % L::kSlots), two ? 1 : 2);   // K is read
+            const int pv = 2 * (j + x - (two ? 1 : 2)) + 1;   // the V of this warpgroup's job before
             if (t.fp8) {
                 if (!cx.warp_wait(L::kScFull + z, use)) return;   // complete: K came after the scales
                 const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
-                if (!softmax_job<D, true>(cx, L::kPvDone + b, pv_parity, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r))
-                    return;
+                if (!softmax_job<D, true>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
             } else {
-                if (!softmax_job<D, false>(cx, L::kPvDone + b, pv_parity, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r))
-                    return;
+                if (!softmax_job<D, false>(cx, pv, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r)) return;
             }
             first = false;
-            ++jobs;
             fence_before();
             mbar_arrive(cx.bar(L::kPFull + b + 2 * buf));
             if (t.fp8) mbar_arrive_n(cx.bar(L::kScFree + z), two ? 1 : 2);   // 256 in all, whoever read them
         }
+        j += n;
         // The segment's partial, a lane a row from here.  With one tile of rows both warpgroups
         // hold half of the tokens: each gets the other's state (through S, idle by then) and adds
         // half of the columns.
@@ -714,9 +667,9 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
         if (live && (two || b == 0)) {
             a.part_ml[at_slot * kRows + row] = make_float2(M, sum);
             // the branch's slots, from its unit's first and last segment
-            const int j = row / d.G;
-            int4* to = a.join + (size_t)(w.branch + rt * a.per_tile + j) * d.hkv + w.row % d.hkv;
-            if (row == j * d.G) {
+            const int br = row / d.G;
+            int4* to = a.join + (size_t)(w.branch + rt * a.per_tile + br) * d.hkv + w.row % d.hkv;
+            if (row == br * d.G) {
                 if (w.flags & kSegFirst) {
                     to->x = w.slot;
                     to->z = rt * kRows + row;
@@ -1001,7 +954,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 4) ||
             (i >= L::kScFull && i < L::kScFull + L::kScales) || i == L::kCvt || i == L::kCvt + 1)
             n = 128;
-        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 17;   // the products, 16 warps
+        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 18;   // the warps that read it
+        if (i >= L::kEmptyB && i < L::kEmptyB + L::kSlots && (i - L::kEmptyB) % 2 == 0) n = 2;
         if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + L::kScales)) n = 256;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1035,7 +989,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             no_prefix(a);
         } else if (warp == 1) {
             pdl_wait();
-            multiply<D>(cx, smem, base, uniform(tmem));
+            multiply_qk<D>(cx, smem, base, uniform(tmem));
+            drain<D>(cx, 0);
+        } else if (warp == 2) {
+            pdl_wait();
+            multiply_pv<D>(cx, smem, base, uniform(tmem));
+            drain<D>(cx, 1);
         }
     } else if (warp < 12) {
         set_regs<128, true>();
