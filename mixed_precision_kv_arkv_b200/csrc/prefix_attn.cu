@@ -17,7 +17,7 @@
 //
 // A CTA: warp 0 walks the run, streams K and V by TMA through a ring of slots (a slot is a
 // tile's K or its V) and hands the segments to the others through shared memory, warps
-// 1 and 2 issue the products, two warpgroups do the softmax, each with its own two S (and P)
+// 1 and 2 issue the products, warp 3 fetches FP8 scales, two warpgroups do the softmax, each with its own two S (and P)
 // and O in tensor memory and its own state, so that neither waits for the other, and two
 // warpgroups rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits), one K,
 // one V.  With one tile of rows the softmax
@@ -88,7 +88,7 @@ struct Smem {
     static constexpr int kQ = 0;                            // two tiles of queries
     static constexpr int kQTile = kRows * D * 2;
     static constexpr int kRing = 2 * kQTile;
-    static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K (log2 units) and V scales
+    static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K and V scales
     static constexpr int kScales = 4;
     static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
     // mbarriers.  K is in the even slots, V in the odd ones.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
@@ -364,47 +364,57 @@ __device__ __forceinline__ void drain(const Ctx& cx, int which) {
     }
 }
 
-// ------------------------------------------------------------------ FP8 -> bf16 (128 threads, two a token)
-// kv = 0: the K tiles and the scales, 1: the V tiles, whose rows past the segment end
-// become zero in either format (stale bits must not meet P = 0).
-template <int D, int FMT>
-__device__ void convert(const AttnArgs& a, const Ctx& cx, char* smem, int ct, int kv) {
+// ------------------------------------------------------------------ FP8 scales (one warp)
+// The K and V scales of every FP8 tile, by asynchronous copies up to kScales tiles ahead of the
+// softmax (which waits a latency of HBM for them otherwise).  Past the end of the row the last
+// token's: what P = 0 meets has to be finite.
+template <int D>
+__device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
     using L = Smem<D>;
-    const LayerDims& d = a.p.d;
-    const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
-    float* scales = reinterpret_cast<float*>(smem + L::kScale);
+    const int lane = threadIdx.x & 31;
+    const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
+    int f = 0;   // FP8 tiles so far
+    Seg w{};
+    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
+        const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
+        const float* sv = a.p.c.sv + (size_t)w.row * a.p.d.cap_q;
+        Tiles tiles(w);
+#pragma unroll 1
+        for (const int end = w.i_end; tiles.i < end;) {
+            const Tile t = tiles.next();
+            if (!t.fp8) continue;
+            const int z = f % L::kScales, use = f / L::kScales;
+            if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // its last readers
+#pragma unroll
+            for (int i = 0; i < 2 * kTok; i += 32) {
+                const int tok = min(t.idx * kTok + (i & (kTok - 1)) + lane, w.n8 - 1);
+                cp_async4(to + 4 * (2 * z * kTok + i), (i < kTok ? sk : sv) + tok);
+            }
+            cp_async_arrive(cx.bar(L::kScFull + z));
+            ++f;
+        }
+    }
+    cp_async_wait_all();
+}
+
+// ------------------------------------------------------------------ FP8 -> bf16 (128 threads, two a token)
+// kv = 0: the K tiles, 1: the V tiles, whose rows past the segment end become zero in either
+// format (stale bits must not meet P = 0).
+template <int D, int FMT>
+__device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
+    using L = Smem<D>;
     const int row = ct >> 1, h = ct & 1;   // token of the tile, half of its dimensions
-    const bool of_v = ct >= kTok;          // the scale that this thread loads: K of token ct, V of ct - 64
-    constexpr int kAhead = 4;              // FP8 tiles between a scale's load and its use (a latency of HBM)
-    int cvt = 0, f = 0, j = 0;   // uses of the read-before-write barrier (D = 64); FP8 tiles, tiles so far
+    int cvt = 0, j = 0;          // uses of the read-before-write barrier (D = 64); tiles so far
     uint32_t raw_ph = 0;         // parity of each slot's next phase (of the K or V loads to convert)
-    Seg w;
+    Seg w{};
     for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
         Tiles tiles(w);
-        float scale[kAhead];     // of the segment's next FP8 tiles
-        auto load_scale = [&](int idx) {
-            const int t = idx * kTok + (ct & (kTok - 1));
-            if (kv == 0 && t < w.n8) return __ldg((of_v ? a.p.c.sv : a.p.c.sk) + (size_t)w.row * d.cap_q + t);
-            return of_v ? 0.f : 1.f;   // past the end: a masked column
-        };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) scale[i] = load_scale(w.f8 + i);
 #pragma unroll 1
         for (const int end = w.i_end; tiles.i < end; ++j) {
             const Tile cur = tiles.next();
-            const int s = (2 * j + kv) % L::kSlots;
             const bool tail = kv == 1 && !cur.fp8 && cur.valid < kTok;
             if (!cur.fp8 && !tail) continue;
-            if (kv == 0) {
-                const int z = f % L::kScales, use = f / L::kScales;
-                if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // their last readers
-                scales[2 * z * kTok + ct] = of_v ? scale[0] : scale[0] * c2;
-                mbar_arrive(cx.bar(L::kScFull + z));
-                ++f;
-#pragma unroll
-                for (int i = 0; i + 1 < kAhead; ++i) scale[i] = scale[i + 1];
-                scale[kAhead - 1] = load_scale(cur.idx + kAhead);
-            }
+            const int s = (2 * j + kv) % L::kSlots;
             if (!cx.warp_wait(L::kRawB + kv * L::kSlots + s, (raw_ph >> s) & 1u)) return;
             raw_ph ^= 1u << s;
             char* slot = smem + L::kRing + s * L::kSlot;
@@ -514,6 +524,19 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
         tmem_ld_16x256b_x8(s, va);
         tmem_ld_16x256b_x8(s + (16u << 16), vb);
         wait_ld(va, vb);
+        if (FP8) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float2 ks = *reinterpret_cast<const float2*>(sk + 8 * g + col);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float* v = (k < 2 ? va : vb) + 4 * g + 2 * (k & 1);
+                    const float2 x = mul2(make_float2(v[0], v[1]), ks);
+                    v[0] = x.x;
+                    v[1] = x.y;
+                }
+            }
+        }
         if (valid < kTok) {   // columns that are no tokens
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -529,19 +552,15 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
         }
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-            float2 ks = make_float2(1.f, 1.f), vs = make_float2(1.f, 1.f);
-            if (FP8) {
-                ks = *reinterpret_cast<const float2*>(sk + 8 * g + col);
-                vs = *reinterpret_cast<const float2*>(sv + 8 * g + col);
-            }
+            float2 vs = make_float2(1.f, 1.f);
+            if (FP8) vs = *reinterpret_cast<const float2*>(sv + 8 * g + col);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float* v = (k < 2 ? va : vb) + 4 * g + 2 * (k & 1);
-                float2 x = make_float2(v[0], v[1]);
-                if (FP8) x = mul2(x, ks);
+                const float2 x = make_float2(v[0], v[1]);
                 mx[k] = fmaxf(fmaxf(mx[k], x.x), x.y);
                 const float2 m2 = make_float2(-r.m[k], -r.m[k]);
-                float2 p = FP8 ? add2(x, m2) : fma2(x, cc, m2);
+                float2 p = fma2(x, cc, m2);
                 p = make_float2(ex2(p.x), ex2(p.y));
                 l[k] = add2(l[k], p);
                 if (FP8) p = mul2(p, vs);
@@ -551,7 +570,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
         bool move = begin;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (!FP8) mx[k] *= c2;
+            mx[k] *= c2;
             r.top[k] = fmaxf(r.top[k], mx[k]);
             move |= mx[k] > r.m[k] + 32.f;
         }
@@ -952,9 +971,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         const int i = tid;
         int n = 1;
         if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 4) ||
-            (i >= L::kScFull && i < L::kScFull + L::kScales) || i == L::kCvt || i == L::kCvt + 1)
+            i == L::kCvt || i == L::kCvt + 1)
             n = 128;
-        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 18;   // the warps that read it
+        if (i >= L::kScFull && i < L::kScFull + L::kScales) n = 32;
+        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 19;   // the warps that read it
         if (i >= L::kEmptyB && i < L::kEmptyB + L::kSlots && (i - L::kEmptyB) % 2 == 0) n = 2;
         if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + L::kScales)) n = 256;
         mbar_init(cx.bar(i), n);
@@ -986,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             produce<D>(a, cx, smem, base, sched);
         } else if (warp == 3) {
             pdl_wait();   // the workspace is the previous call's until it has finished
+            load_scales<D>(a, cx, smem);
             no_prefix(a);
         } else if (warp == 1) {
             pdl_wait();
@@ -1003,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     } else {
         set_regs<72, false>();
         pdl_wait();
-        convert<D, FMT>(a, cx, smem, tid & 127, (warp - 12) >> 2);
+        convert<D, FMT>(cx, smem, tid & 127, (warp - 12) >> 2);
     }
     __syncwarp();
     fence_before();
