@@ -1050,8 +1050,10 @@ __global__ void __launch_bounds__(4 * D) prefix_join_kernel(const __grid_constan
     const int b = divided(blockIdx.x, a.div_hkv), g = blockIdx.x - b * d.hkv;
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
     const size_t mi = (size_t)blockIdx.x * 4 + jq, at = (((size_t)b * d.hq + g * d.G + jq) * D) / 4 + c4;
-    pdl_launch_dependents();
     pdl_wait();
+    // Only now may the next kernel start: what came before the attention kernel is then complete
+    // and visible to whatever that kernel reads ahead of its own wait.
+    pdl_launch_dependents();
     const int4 info = __ldcg(a.join + blockIdx.x);
     float M = kNegInf, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
