@@ -62,8 +62,11 @@ class Workspace:
 
 
 def stream_ptr(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    """The raw handle of `stream`, or of the current device's current stream (without the stream
+    object that torch.cuda.current_stream() makes: 0.2 us instead of 3.3)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 @dataclass
@@ -100,8 +103,8 @@ def decode_step(st: LayerState, step: int, q, k_new, v_new, ctx_len, o, reassign
 
 def _on_device(t: torch.Tensor, stream):
     """The device guard and raw stream of a call on t's device."""
-    s = stream if stream is not None else torch.cuda.current_stream(t.device)
-    return torch.cuda.device(t.device), s.cuda_stream
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch.cuda.device(t.device), s
 
 
 def _ptr(t):

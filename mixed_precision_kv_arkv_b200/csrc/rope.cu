@@ -6,14 +6,15 @@
 // so a thread keeps two factors for each of its 8 dimensions (cos and sin with the weights
 // folded in) and reuses them for all the heads of its token that it takes.
 //
-// A group of D / 8 threads takes a head, 16 bytes a thread; a block's groups are dealt to 4
-// tokens (1 when there are few, so that a decode step still fills the GPU), and each group
-// takes every n-th head of its token, four loads in flight.  Sines and cosines are computed
+// A group of D / 8 threads takes a head, 16 bytes a thread; a block's groups are dealt to its
+// tokens, and each group takes every n-th head of its token, four loads in flight.  The
+// arithmetic is on packed pairs.  Sines and cosines are computed
 // once a token and pair, into shared memory: the angle in turns as a 64-bit fraction,
 // position * round(freq / 2 pi * 2^64) modulo 2^64, is exact for any position.
 //
 // Bound: HBM, every projection row read and every output written once.  8192 tokens of 48
-// heads of 128: 201.9 MB, floor 31.2 us at 6461.5 GB/s; MEASURED_LINE
+// heads of 128: 201.9 MB, floor 31.2 us at 6461.5 GB/s; 43.9 us measured (4.6 TB/s; the
+// loads' and shuffles' latencies at 32 warps an SM and half of the issue slots are what is left).
 #include "arkv_internal.cuh"
 #include "tc.cuh"
 
@@ -23,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;   // heads of a group in flight
+constexpr int kMaxTokens = 16;
 
 enum { kHalf = 0, kInterleaved = 1, kOdd = 2 };   // pairs (i, i + rot / 2), whole vectors apart; (2i, 2i + 1); any rot
 
@@ -42,9 +44,9 @@ __device__ __forceinline__ float2 turn(int64_t pos, double freq) {
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p, int tokens) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeParams p, int tokens) {
     constexpr int kGroup = D / 8, kGroups = kThreads / kGroup;
-    __shared__ float2 sm_turn[4][D / 2];
+    __shared__ __align__(16) float2 sm_turn[kMaxTokens][D / 2];
     const LayerDims& d = p.d;
     const int tid = threadIdx.x, gl = tid % kGroup, group = tid / kGroup;
     const int half = p.rot / 2, total = d.batch * p.n_tok;
@@ -71,114 +73,151 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     int partner = gl;                               // the thread that holds the partners of these dimensions
     if (MODE == kHalf && dim0 < p.rot) partner = dim0 < half ? gl + half / 8 : gl - half / 8;
 
-    // factors of this thread's dimensions for queries (kind 0), then keys (1)
-    float fc[8], fs[8];
+    // factors of this thread's dimensions for queries, then keys: pairs of dimensions
+    float2 fc[4], fs[4];
     auto partner_dim = [&](int i) {
         if (i >= p.rot) return i;
         if (MODE == kInterleaved) return i ^ 1;
         return i < half ? i + half : i - half;
     };
     auto factors = [&](const uint16_t* w) {
+        float c[8], v[8], wo[8], wp[8];
+        const bool rotated = dim0 < p.rot;
+        if (MODE == kHalf) {   // whole vectors: pairs j0 .. j0 + 7, partners dim0 +- half ..
+            const int j0 = dim0 < half ? dim0 : dim0 - half;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = dim0 + e;
-            float c = 1.f, s = 0.f;
-            if (i < p.rot) {
-                const int j = MODE == kInterleaved ? i >> 1 : (i < half ? i : i - half);
-                const float2 cs = sm_turn[lt][j];
-                const bool a = MODE == kInterleaved ? !(e & 1) : i < half;
-                c = cs.x;
-                s = a ? -cs.y : cs.y;
+            for (int e = 0; e < 4; ++e) {
+                const float4 cs = rotated ? *reinterpret_cast<const float4*>(&sm_turn[lt][j0 + 2 * e])
+                                          : make_float4(1.f, 0.f, 1.f, 0.f);
+                c[2 * e] = cs.x; c[2 * e + 1] = cs.z;
+                v[2 * e] = dim0 < half ? -cs.y : cs.y; v[2 * e + 1] = dim0 < half ? -cs.w : cs.w;
             }
-            fc[e] = w ? c * bf16_to_f32(w[i]) : c;
-            fs[e] = w ? s * bf16_to_f32(w[partner_dim(i)]) : s;
-        }
-    };
-    auto head_out = [&](int h, const uint4& y) {
-        const int64_t at = ((int64_t)t) * D + dim0;
-        if (h < d.hq) {
-            if (p.q) *reinterpret_cast<uint4*>(p.q + ((int64_t)b * d.hq + h) * p.n_stride * D + at) = y;
-            const int o = t - (len - d.n_obs);
-            if (p.q_obs && o >= 0)
-                *reinterpret_cast<uint4*>(p.q_obs + (((int64_t)b * d.hq + h) * d.n_obs + o) * D + dim0) = y;
         } else {
-            const int kv = h - d.hq, g = kv < d.hkv ? kv : kv - d.hkv;
-            *reinterpret_cast<uint4*>((kv < d.hkv ? p.k : p.v) + ((int64_t)b * d.hkv + g) * p.n_stride * D + at) = y;
-        }
-    };
-    // heads [lo, hi) of one kind, kUnroll at a time
-    auto run = [&](int lo, int hi, bool norm) {
-        for (int h0 = lo; h0 < hi; h0 += kUnroll * stride) {
-            uint4 raw[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int h = h0 + u * stride;
-                raw[u] = h < hi ? __ldcs(reinterpret_cast<const uint4*>(x_row + (int64_t)h * D + dim0)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < 8; ++e) {
+                const int i = dim0 + e;
+                const bool in = i < p.rot;
+                const float2 cs = in ? sm_turn[lt][MODE == kInterleaved ? i >> 1 : (i < half ? i : i - half)] : make_float2(1.f, 0.f);
+                c[e] = cs.x;
+                v[e] = (MODE == kInterleaved ? !(e & 1) : i < half) ? -cs.y : cs.y;
             }
+        }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int h = h0 + u * stride;
-                if (h >= hi) break;
-                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-                float x[8], y[8];
-                float ss = 0.f;
+        for (int e = 0; e < 8; ++e) wo[e] = wp[e] = 1.f;
+        if (w) {
+            if (MODE == kHalf && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+                const uint4 a = *reinterpret_cast<const uint4*>(w + dim0);
+                const uint4 q = *reinterpret_cast<const uint4*>(w + (rotated ? partner_dim(dim0) : dim0));
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = bf16_lo(w[e]);
-                    x[2 * e + 1] = bf16_hi(w[e]);
-                    ss = fmaf(x[2 * e], x[2 * e], fmaf(x[2 * e + 1], x[2 * e + 1], ss));
+                    wo[2 * e] = bf16_lo(aw[e]); wo[2 * e + 1] = bf16_hi(aw[e]);
+                    wp[2 * e] = bf16_lo(qw[e]); wp[2 * e + 1] = bf16_hi(qw[e]);
                 }
-                float inv = 1.f;
-                if (norm) {
+            } else {
 #pragma unroll
-                    for (int m = kGroup / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
-                    inv = rsqrtf(ss * (1.f / D) + p.eps);
+                for (int e = 0; e < 8; ++e) {
+                    wo[e] = bf16_to_f32(w[dim0 + e]);
+                    wp[e] = bf16_to_f32(w[partner_dim(dim0 + e)]);
                 }
-                if (MODE == kInterleaved) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = inv * fmaf(x[e], fc[e], dim0 + e < p.rot ? x[e ^ 1] * fs[e] : 0.f);
-                } else {
-                    float z[8];
-                    if (MODE == kHalf) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t o = __shfl_sync(mask, w[e], partner, kGroup);
-                            if (dim0 >= p.rot) o = 0u;   // not rotated: rot is a multiple of 16 here
-                            z[2 * e] = bf16_lo(o);
-                            z[2 * e + 1] = bf16_hi(o);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            z[e] = dim0 + e < p.rot ? bf16_to_f32(x_row[(int64_t)h * D + partner_dim(dim0 + e)]) : 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = inv * fmaf(x[e], fc[e], z[e] * fs[e]);
-                }
-                head_out(h, make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])));
             }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            fc[e] = make_float2(c[2 * e] * wo[2 * e], c[2 * e + 1] * wo[2 * e + 1]);
+            fs[e] = make_float2(v[2 * e] * wp[2 * e], v[2 * e + 1] * wp[2 * e + 1]);
+        }
+    };
+    // Heads first, first + stride, .. below hi: head h goes to out + (h - h_base) * step, and to
+    // obs + (h - h_base) * obs_step (a query of the last positions).
+    auto run = [&](int h, int hi, const uint16_t* w, uint16_t* out, int64_t step, uint16_t* obs, int64_t obs_step) {
+        const uint4* src = reinterpret_cast<const uint4*>(x_row + (int64_t)h * D + dim0);
+        const int src_step = stride * (D / 8);
+        auto one = [&](const uint4& raw, int hh, int u) {
+            const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+            float2 x[4], y[4];
+            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = make_float2(bf16_lo(r[e]), bf16_hi(r[e]));
+            float inv = 1.f;
+            if (w) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ss = tc::fma2(x[e], x[e], ss);
+                float t = ss.x + ss.y;
+#pragma unroll
+                for (int m = kGroup / 2; m >= 1; m >>= 1) t += __shfl_xor_sync(mask, t, m);
+                inv = rsqrtf(fmaf(t, 1.f / D, p.eps));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 z;
+                if (MODE == kInterleaved) {
+                    z = dim0 + 2 * e < p.rot ? make_float2(x[e].y, x[e].x) : make_float2(0.f, 0.f);
+                } else if (MODE == kHalf) {
+                    uint32_t o = __shfl_sync(mask, r[e], partner, kGroup);
+                    if (dim0 >= p.rot) o = 0u;   // not rotated: rot is a multiple of 16 here
+                    z = make_float2(bf16_lo(o), bf16_hi(o));
+                } else {
+                    const int i = dim0 + 2 * e;
+                    const uint16_t* from = x_row + (int64_t)hh * D;
+                    z.x = i < p.rot ? bf16_to_f32(from[partner_dim(i)]) : 0.f;
+                    z.y = i + 1 < p.rot ? bf16_to_f32(from[partner_dim(i + 1)]) : 0.f;
+                }
+                y[e] = tc::fma2(x[e], fc[e], tc::mul2(z, fs[e]));
+                if (w) y[e] = tc::mul2(y[e], make_float2(inv, inv));
+            }
+            const uint4 v = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y), pack2(y[2].x, y[2].y), pack2(y[3].x, y[3].y));
+            if (out) *reinterpret_cast<uint4*>(out + u * step) = v;
+            if (obs) *reinterpret_cast<uint4*>(obs + u * obs_step) = v;
+        };
+        for (; h + (kUnroll - 1) * stride < hi; h += kUnroll * stride) {
+            uint4 raw[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) raw[u] = __ldcs(src + u * src_step);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) one(raw[u], h + u * stride, u);
+            src += kUnroll * src_step;
+            if (out) out += kUnroll * step;
+            if (obs) obs += kUnroll * obs_step;
+        }
+        for (; h < hi; h += stride) {
+            one(__ldcs(src), h, 0);
+            src += src_step;
+            if (out) out += step;
+            if (obs) obs += obs_step;
         }
     };
     auto begin = [&](int from) {   // this group's first head at or after `from`
         const int k = from <= first ? 0 : (from - first + stride - 1) / stride;
         return first + k * stride;
     };
-    if (p.q || (p.q_obs && t >= len - d.n_obs)) {
+    const int64_t head_step = (int64_t)p.n_stride * D, at = (int64_t)t * D + dim0;
+    const int o = t - (len - d.n_obs);
+    if (p.q || (p.q_obs && o >= 0)) {
+        const int h = begin(0);
         factors(p.q_weight);
-        run(begin(0), d.hq, p.q_weight != nullptr);
+        run(h, d.hq, p.q_weight, p.q ? p.q + ((int64_t)b * d.hq + h) * head_step + at : nullptr, stride * head_step,
+            p.q_obs && o >= 0 ? p.q_obs + (((int64_t)b * d.hq + h) * d.n_obs + o) * D + dim0 : nullptr,
+            (int64_t)stride * d.n_obs * D);
     }
-    factors(p.k_weight);
-    run(begin(d.hq), heads, p.k_weight != nullptr);
-    for (int h0 = begin(heads); h0 < heads + d.hkv; h0 += kUnroll * stride) {   // values: a copy
+    {
+        const int h = begin(d.hq);
+        factors(p.k_weight);
+        run(h, heads, p.k_weight, p.k + ((int64_t)b * d.hkv + h - d.hq) * head_step + at, stride * head_step, nullptr, 0);
+    }
+    int h = begin(heads);   // values: a copy
+    const uint4* src = reinterpret_cast<const uint4*>(x_row + (int64_t)h * D + dim0);
+    uint16_t* out = p.v + ((int64_t)b * d.hkv + h - heads) * head_step + at;
+    for (; h < heads + d.hkv; h += kUnroll * stride) {
         uint4 raw[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            if (h0 + u * stride < heads + d.hkv)
-                raw[u] = __ldcs(reinterpret_cast<const uint4*>(x_row + (int64_t)(h0 + u * stride) * D + dim0));
+            if (h + u * stride < heads + d.hkv) raw[u] = __ldcs(src + u * stride * (D / 8));
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            if (h0 + u * stride < heads + d.hkv) head_out(h0 + u * stride, raw[u]);
+            if (h + u * stride < heads + d.hkv) *reinterpret_cast<uint4*>(out + u * stride * head_step) = raw[u];
+        src += kUnroll * stride * (D / 8);
+        out += kUnroll * stride * head_step;
     }
 }
 
@@ -188,10 +227,12 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s) {
     const LayerDims& d = p.d;
     const long long total = (long long)d.batch * p.n_tok;
     const int groups = kThreads / (d.D / 8);
-    // 4 tokens a block share the block's start; with fewer than about four blocks an SM that
-    // way, a token gets the whole block, or several (a head a group and no more).
-    // ROPE_SPLIT_NOTE
-    const int tokens = total >= 4 * 4 * 148 ? 4 : 1;
+    // A group's start (its factors) is shared by all the heads it takes, so a block takes as many
+    // tokens as leave a group 48 heads, or two blocks an SM (8192 tokens of 48 heads: 2 tokens a
+    // block 67 us, 4 54, 8 45, 16 44; 6964 of 12 heads of 64: 4 tokens 15, 16 10.8).  A call of
+    // few tokens gives each a block, or several (at most a head a group), up to two an SM.
+    int tokens = 1;
+    while (tokens < kMaxTokens && (d.hq + 2 * d.hkv) * tokens < groups * 48 && total >= 2ll * 148 * tokens) tokens *= 2;
     const int per = groups / tokens, heads = d.hq + 2 * d.hkv;
     long long split = 1;
     while (tokens == 1 && total * split < 2 * 148 && split * per < heads) ++split;
