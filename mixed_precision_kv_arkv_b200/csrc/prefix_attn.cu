@@ -7,9 +7,9 @@
 //   S[128 rows][64 tokens] = Q K^T,   O[128 rows][D] += P V,   P = 2^(S c - m).
 //
 // Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 64 tokens
-// are the bf16 and the FP8 tiles of the prefix row, interleaved evenly, because an FP8
-// tile has twice the arithmetic per byte.  The tiles of all units form one list, cut into
-// equal runs, one a CTA and one CTA an SM; a run that crosses units is several segments,
+// are the bf16 and the FP8 tiles of the prefix row.  The tiles of all units form one list,
+// cut into equal runs, one a CTA and one CTA an SM (with shares of a unit's bf16 and FP8 tiles
+// in proportion: an FP8 tile has twice the arithmetic per byte); a run that crosses units is several segments,
 // each with a partial (max, sum, unnormalised o) in the workspace.  In the list every unit
 // begins with kSegCost empty places, about what the start of another segment costs, so
 // that the run that holds them has that many tiles less.
@@ -26,15 +26,16 @@
 // both.  Either way a softmax job is one S, and the jobs alternate.
 // P takes the place of S.  The K scale of an FP8 token enters the exponent's factor, its V
 // scale is folded into P.
-// The softmax reference m is the maximum of a segment's first tile and moves only when a
-// logit exceeds it by 2^32 (float32 and bf16 have the range), so O is hardly ever rescaled
-// and a job needs no maximum before its exponentials.  P is rounded to bf16 once, the rounding that o itself gets; the
+// The softmax reference m starts as zero and moves only when a logit exceeds it by 2^32 (or
+// the first tile's are all as far below: float32 and bf16 have the range), so O is hardly ever
+// rescaled and a job needs no maximum before its exponentials.  P is rounded to bf16 once, the rounding that o itself gets; the
 // sum is of the unrounded values.
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
 // memory is freed and the call ends.
 #include <math.h>
 #include <mutex>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -68,26 +69,27 @@ struct Sched {
     RowInfo r;
 };
 
-// A segment: tiles [i, i_end) of a unit of T tiles, T8 of them FP8, and the interleave's
-// state at tile i (f8 FP8 tiles before it).
+// A segment: tiles [i16, e16) of the row's bf16 tiles, then those from i8 on of its FP8 tiles, n in
+// all.
 enum : int { kSegFirst = 1, kSegLast = 2, kSegTwo = 4, kSegEnd = 8 };
 struct Seg {
-    int row, n16, n8, T, T8, i, i_end, f8, err;
+    int row, n16, n8, n, i16, e16, i8;
     int branch, rows0, rows1;   // first branch; live rows of the two tiles of rows
     int slot, flags;            // place of its partial; first, last of its unit, two tiles of rows, no segment
 };
 
 // ------------------------------------------------------------------ shared memory
-template <int D>
+// TWO: room for two tiles of queries (else one, and a tile of tokens more in the ring).
+template <int D, bool TWO>
 struct Smem {
-    static constexpr int kSlots = 10;                       // five tiles
+    static constexpr int kSlots = TWO ? 10 : 12;            // five or six tiles
     static constexpr int kSegs = 2;                         // segments on their way from the scheduler
     static constexpr int kSlot = kTok * D * 2;              // a K or V tile in bf16
     static constexpr int kRegion = kTok * 128;              // 64 dimensions of it (128-byte rows, swizzled)
     static constexpr int kRaw = D == 64 ? kSlot / 2 : 0;    // where in its slot an FP8 tile lands
-    static constexpr int kQ = 0;                            // two tiles of queries
+    static constexpr int kQ = 0;
     static constexpr int kQTile = kRows * D * 2;
-    static constexpr int kRing = 2 * kQTile;
+    static constexpr int kRing = (TWO ? 2 : 1) * kQTile;
     static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K and V scales
     static constexpr int kScales = 4;
     static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
@@ -174,25 +176,19 @@ struct Tile {
     int fp8, idx, valid;   // kind, place in its row's segment of the cache, live tokens
 };
 
-// The tiles of a segment in order: after i tiles of a unit, floor(i T8 / T) are FP8.
+// The tiles of a segment in order: the bf16 tiles first.  (Alternating the two kinds made the
+// softmax warps fetch their code anew all the time: 64 us against 50 for a 131072-token prefix
+// and 32 branches.)
 struct Tiles {
-    int i, n16, n8, T, T8, f8, err;
+    int n, i16, e16, i8, n16, n8;
     __device__ __forceinline__ explicit Tiles(const Seg& s)   // (a whole warp)
-        : i(uniform(s.i)), n16(uniform(s.n16)), n8(uniform(s.n8)), T(uniform(s.T)), T8(uniform(s.T8)), f8(uniform(s.f8)),
-          err(uniform(s.err)) {}
+        : n(uniform(s.n)), i16(uniform(s.i16)), e16(uniform(s.e16)), i8(uniform(s.i8)), n16(uniform(s.n16)),
+          n8(uniform(s.n8)) {}
     __device__ __forceinline__ Tile next() {
         Tile x;
-        err += T8;
-        x.fp8 = err >= T;
-        if (x.fp8) {
-            err -= T;
-            x.idx = f8++;
-            x.valid = min(kTok, n8 - x.idx * kTok);
-        } else {
-            x.idx = i - f8;
-            x.valid = min(kTok, n16 - x.idx * kTok);
-        }
-        ++i;
+        x.fp8 = i16 >= e16;
+        x.idx = x.fp8 ? i8++ : i16++;
+        x.valid = min(kTok, (x.fp8 ? n8 : n16) - x.idx * kTok);
         return x;
     }
 };
@@ -218,10 +214,16 @@ struct Ctx {
     __device__ __forceinline__ bool warp_wait(int i, uint32_t parity) const { return __all_sync(kFull, wait(i, parity)); }
 };
 
+// One arrival for a warp, after all its lanes (n: counted n times).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, uint32_t n = 1) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_n(bar, n);
+}
+
 // Segment number `seg` from the scheduler, to a warp; false at the end of the run.
-template <int D>
+template <int D, bool TWO>
 __device__ __forceinline__ bool warp_segment(const Ctx& cx, const char* smem, int seg, Seg& out) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     const int z = seg % L::kSegs;
     if (!cx.warp_wait(L::kSegFull + z, (seg / L::kSegs) & 1)) return false;
     out = *reinterpret_cast<const Seg*>(smem + L::kSeg + z * 64);
@@ -268,19 +270,19 @@ __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 6
 // follows the completion of P V of job x - 4, which read P from the same place.  (With one warp
 // for both, polling for whichever was ready, a tile of 64 took 0.5 us more: it shares its
 // scheduler with four busy warps, and its instructions were what a tile waited for.)
-template <int D>
+template <int D, bool TWO>
 __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false);
     int j = 0;                     // tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
     Seg w{};
-    for (int seg = 0; warp_segment<D>(cx, gsmem, seg, w); ++seg) {
+    for (int seg = 0; warp_segment<D, TWO>(cx, gsmem, seg, w); ++seg) {
         Tiles tiles(w);
-        const bool two = uniform(w.flags) & kSegTwo;
-        const int sh = two ? 1 : 0, n = uniform(w.i_end) - tiles.i, jobs = n << sh;
+        const bool two = TWO && (uniform(w.flags) & kSegTwo);
+        const int sh = two ? 1 : 0, n = tiles.n, jobs = n << sh;
         if (!cx.warp_wait(L::kQFull, seg & 1) || (seg > 0 && !cx.warp_wait(L::kEpi, (seg - 1) & 1))) return;
 #pragma unroll 1
         for (int x = 0; x < jobs; ++x) {
@@ -312,19 +314,19 @@ __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uin
     }
 }
 
-template <int D>
+template <int D, bool TWO>
 __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     constexpr uint32_t kIdPV = idesc_bf16(kRows, D, true);
     int j = 0;                     // tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
     uint32_t p_ph = 0;             // parity of the next P of each of the four S
     const bool leader = elect_one();
     Seg w{};
-    for (int seg = 0; warp_segment<D>(cx, gsmem, seg, w); ++seg) {
+    for (int seg = 0; warp_segment<D, TWO>(cx, gsmem, seg, w); ++seg) {
         Tiles tiles(w);
-        const bool two = uniform(w.flags) & kSegTwo;
-        const int sh = two ? 1 : 0, n = uniform(w.i_end) - tiles.i, jobs = n << sh;
+        const bool two = TWO && (uniform(w.flags) & kSegTwo);
+        const int sh = two ? 1 : 0, n = tiles.n, jobs = n << sh;
 #pragma unroll 1
         for (int x = 0; x < jobs; ++x) {
             const int b = x & 1, z = x & 3, e = 2 * (j + (x >> sh)) + 1, s = e % L::kSlots;
@@ -355,9 +357,9 @@ __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uin
 }
 
 // Waits until every product of this warp has completed (before tensor memory is freed).
-template <int D>
+template <int D, bool TWO>
 __device__ __forceinline__ void drain(const Ctx& cx, int which) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     if (elect_one()) commit(cx.bar(L::kFin + which));
     __syncwarp();
     for (int z = 0; z < kSpinLimit && !mbar_try_wait(cx.bar(L::kFin + which), 0); ++z) {
@@ -368,19 +370,19 @@ __device__ __forceinline__ void drain(const Ctx& cx, int which) {
 // The K and V scales of every FP8 tile, by asynchronous copies up to kScales tiles ahead of the
 // softmax (which waits a latency of HBM for them otherwise).  Past the end of the row the last
 // token's: what P = 0 meets has to be finite.
-template <int D>
+template <int D, bool TWO>
 __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     const int lane = threadIdx.x & 31;
     const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
     int f = 0;   // FP8 tiles so far
     Seg w{};
-    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
+    for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
         const float* sv = a.p.c.sv + (size_t)w.row * a.p.d.cap_q;
         Tiles tiles(w);
 #pragma unroll 1
-        for (const int end = w.i_end; tiles.i < end;) {
+        for (int i = 0; i < tiles.n; ++i) {
             const Tile t = tiles.next();
             if (!t.fp8) continue;
             const int z = f % L::kScales, use = f / L::kScales;
@@ -400,17 +402,17 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
 // ------------------------------------------------------------------ FP8 -> bf16 (128 threads, two a token)
 // kv = 0: the K tiles, 1: the V tiles, whose rows past the segment end become zero in either
 // format (stale bits must not meet P = 0).
-template <int D, int FMT>
+template <int D, int FMT, bool TWO>
 __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     const int row = ct >> 1, h = ct & 1;   // token of the tile, half of its dimensions
     int cvt = 0, j = 0;          // uses of the read-before-write barrier (D = 64); tiles so far
     uint32_t raw_ph = 0;         // parity of each slot's next phase (of the K or V loads to convert)
     Seg w{};
-    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
+    for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         Tiles tiles(w);
 #pragma unroll 1
-        for (const int end = w.i_end; tiles.i < end; ++j) {
+        for (const int end = j + tiles.n; j < end; ++j) {
             const Tile cur = tiles.next();
             const bool tail = kv == 1 && !cur.fp8 && cur.valid < kTok;
             if (!cur.fp8 && !tail) continue;
@@ -433,7 +435,7 @@ __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
                     if (zero) raw[c] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 if constexpr (D == 64) {
-                    mbar_arrive(cx.bar(L::kCvt + kv));
+                    warp_arrive(cx.bar(L::kCvt + kv));
                     if (!cx.warp_wait(L::kCvt + kv, cvt++ & 1)) return;
                 } else {
                     __syncwarp();
@@ -457,7 +459,7 @@ __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
                         make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async();
-            mbar_arrive(cx.bar(L::kConvB + s));
+            warp_arrive(cx.bar(L::kConvB + s));
         }
     }
 }
@@ -509,10 +511,10 @@ __device__ __noinline__ void rescale(uint32_t o, float ff) {
 
 // One job: S at column s of the warp's lanes becomes P.  The whole tile is one piece of code
 // (the exponentials set its pace, and everything else has to fit between them), which is run
-// again when the reference turns out too low -- rarely, and on the first job of a segment, when
-// there is none yet.  O (column o) then has to be idle: the product of the job before has
+// again when the reference turns out wrong: too low, or, in a segment's first job, which starts
+// from zero, too high.  O (column o) then has to be idle: the product of the job before has
 // completed when it frees its V, entry pv.  False if that took too long.
-template <int D, bool FP8>
+template <int D, bool FP8, bool TWO>
 __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, uint32_t o, bool first, int valid,
                                             const float* sk, const float* sv, float c2, Rows& r) {
     const float2 cc = make_float2(c2, c2);
@@ -567,14 +569,15 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
                 (k < 2 ? pa : pb)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
             }
         }
-        bool move = begin;
+        bool move = false, low = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             mx[k] *= c2;
             r.top[k] = fmaxf(r.top[k], mx[k]);
             move |= mx[k] > r.m[k] + 32.f;
+            if (begin) low |= quad_max(mx[k]) < -32.f;
         }
-        if (!__any_sync(kFull, move)) {
+        if (!__any_sync(kFull, move || low)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) r.l[k] += l[k].x + l[k].y;
             tmem_st_16x128b_x8(s, pa);   // over S, which has been read
@@ -587,7 +590,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
         for (int k = 0; k < 4; ++k) {
             const float t = quad_max(mx[k]);
             if (begin) {
-                r.m[k] = t == kNegInf ? 0.f : t;
+                r.m[k] = t != kNegInf && fabsf(t) > 32.f ? t : 0.f;   // (each row for itself)
             } else {
                 const float up = fmaxf(ceilf(t - r.m[k]), 0.f);
                 f[k] = ex2(-up);
@@ -596,7 +599,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
             }
         }
         if (!begin) {
-            if (!cx.warp_wait(Smem<D>::kEmptyB + pv % Smem<D>::kSlots, (pv / Smem<D>::kSlots) & 1)) return false;
+            if (!cx.warp_wait(Smem<D, TWO>::kEmptyB + pv % Smem<D, TWO>::kSlots, (pv / Smem<D, TWO>::kSlots) & 1)) return false;
             fence_after();
             rescale<D>(o, row_value(f));
         }
@@ -604,20 +607,22 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
     }
 }
 
-template <int D>
+template <int D, bool TWO>
 __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t tmem, int b) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     const LayerDims& d = a.p.d;
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const uint32_t lane = tmem + ((uint32_t)(quad * 32) << 16), s = lane + tmem_s(b, 0), o = lane + tmem_o<D>(b);
     const float c2 = (float)(a.p.inv_sqrt_d * 1.4426950408889634);
     int f = 0, xch = 0, j = 0;      // FP8 tiles, exchanges and tiles so far
     uint32_t s_ph = 0;              // parity of the next of each of its two S
-    Seg w;
-    for (int seg = 0; warp_segment<D>(cx, smem, seg, w); ++seg) {
-        const bool two = w.flags & kSegTwo;
-        const int n = w.i_end - w.i;
+    for (int seg = 0;; ++seg) {
+        // (what the end of the segment needs stays in shared memory until then)
+        const Seg& w = *reinterpret_cast<const Seg*>(smem + L::kSeg + seg % L::kSegs * 64);
+        if (!cx.warp_wait(L::kSegFull + seg % L::kSegs, (seg / L::kSegs) & 1) || (w.flags & kSegEnd)) return;
+        const bool two = TWO && (w.flags & kSegTwo);
         Tiles tiles(w);
+        const int n = tiles.n;
         Rows r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -641,14 +646,14 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             if (t.fp8) {
                 if (!cx.warp_wait(L::kScFull + z, use)) return;   // complete: K came after the scales
                 const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
-                if (!softmax_job<D, true>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
+                if (!softmax_job<D, true, TWO>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
             } else {
-                if (!softmax_job<D, false>(cx, pv, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r)) return;
+                if (!softmax_job<D, false, TWO>(cx, pv, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r)) return;
             }
             first = false;
             fence_before();
-            mbar_arrive(cx.bar(L::kPFull + b + 2 * buf));
-            if (t.fp8) mbar_arrive_n(cx.bar(L::kScFree + z), two ? 1 : 2);   // 256 in all, whoever read them
+            warp_arrive(cx.bar(L::kPFull + b + 2 * buf));
+            if (t.fp8) warp_arrive(cx.bar(L::kScFree + z), two ? 1 : 2);   // 8 in all, whoever read them
         }
         j += n;
         // The segment's partial, a lane a row from here.  With one tile of rows both warpgroups
@@ -667,7 +672,7 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             tmem_st4(s, m, my_top, my_l, 0.f);
             wait_st();
             fence_before();
-            mbar_arrive(cx.bar(L::kXch));
+            warp_arrive(cx.bar(L::kXch));
             if (!cx.warp_wait(L::kXch, xch++ & 1)) return;
             fence_after();
             tmem_ld4(lane + tmem_s(b ^ 1, 0), y);
@@ -716,7 +721,8 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             }
         }
         fence_before();
-        mbar_arrive(cx.bar(L::kEpi));
+        warp_arrive(cx.bar(L::kEpi));
+        warp_arrive(cx.bar(L::kSegEmpty + seg % L::kSegs));
     }
 }
 
@@ -784,9 +790,9 @@ __device__ __forceinline__ Sched find_run(const AttnArgs& a) {
 // Walks the run (one warp, one lane of which issues): loads every segment's tiles and queries, and publishes the
 // segment once its first loads are on their way (the other roles need it, and their code,
 // only when those land).
-template <int D>
+template <int D, bool TWO>
 __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t smem, Sched s) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     const LayerDims& d = a.p.d;
     const int per_unit = a.row_tiles * a.per_tile;
     int seg = 0, e = 0, m = 0;              // segments and entries so far; place of the unit in its row
@@ -831,6 +837,7 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
     for (;;) {
         // the next segment
         bool any = false;
+        int t0 = 0, t1 = 0;   // the run's tiles of the unit
         while (ok && !any && s.v < s.v_end) {
             while (s.v >= s.base + T + kSegCost) {   // the unit that holds place v
                 s.base += T + kSegCost;
@@ -849,10 +856,10 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
                 if (s.v >= s.v_end) break;
             }
             if (s.v >= s.v_end) break;
-            x.i = max(s.v - s.base - kSegCost, 0);
-            x.i_end = min(s.v_end - s.base - kSegCost, T);
+            t0 = max(s.v - s.base - kSegCost, 0);
+            t1 = min(s.v_end - s.base - kSegCost, T);
             s.v = min(s.base + kSegCost + T, s.v_end);
-            any = x.i < x.i_end;
+            any = t0 < t1;
         }
         const int z = seg % L::kSegs;
         Seg* out = reinterpret_cast<Seg*>(gsmem + L::kSeg + z * 64);
@@ -864,22 +871,25 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
             }
             break;
         }
-        x.f8 = x.i == 0 ? 0 : T < 65536 ? (int)((unsigned)x.i * r.T8 / (unsigned)T) : (int)((long long)x.i * r.T8 / T);
-        x.err = (int)((long long)x.i * r.T8 - (long long)x.f8 * T);
+        // a share of the bf16 and of the FP8 tiles in proportion: of t tiles, floor(t T8 / T) are FP8
+        auto fp8_of = [&](int t) { return T < 65536 ? (int)((unsigned)t * r.T8 / (unsigned)T) : (int)((long long)t * r.T8 / T); };
+        const int f0 = t0 == 0 ? 0 : fp8_of(t0), f1 = t1 == T ? r.T8 : fp8_of(t1);
+        x.n = t1 - t0;
+        x.i16 = t0 - f0;
+        x.e16 = t1 - f1;
+        x.i8 = f0;
         x.row = s.row;
         x.n16 = r.n16;
         x.n8 = r.n8;
-        x.T = T;
-        x.T8 = r.T8;
         const int left = r.nb - m * per_unit;
         x.branch = r.b0 + m * per_unit;
-        x.flags = (x.i == 0 ? kSegFirst : 0) | (x.i_end == T ? kSegLast : 0) |
+        x.flags = (t0 == 0 ? kSegFirst : 0) | (t1 == T ? kSegLast : 0) |
                   (a.row_tiles > 1 && left > a.per_tile ? kSegTwo : 0);
         // The segment's queries follow its first tiles: an early-started call fills its whole
         // ring before the wait for the previous kernel, and a later segment's queries wait
         // until the products of the one before have read theirs, which its first tile need not.
         Tiles tiles(x);
-        const int n = x.i_end - x.i, ahead = min(n, seg == 0 && a.p.early_start ? L::kSlots / 2 : 1);
+        const int n = x.n, ahead = min(n, seg == 0 && a.p.early_start ? L::kSlots / 2 : 1);
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
             const Tile t = tiles.next();
@@ -890,7 +900,7 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
                 waited = true;
             }
             if (seg > 0 && !(ok = cx.warp_wait(L::kQEmpty, (seg - 1) & 1))) continue;
-            const int count = x.flags & kSegTwo ? 2 : 1, head = x.row - divided(x.row, a.div_hkv) * d.hkv;
+            const int count = TWO && (x.flags & kSegTwo) ? 2 : 1, head = x.row - divided(x.row, a.div_hkv) * d.hkv;
             if (leader) {
                 mbar_expect_tx(cx.bar(L::kQFull), count * a.per_tile * d.G * D * 2);
 #pragma unroll 1
@@ -951,9 +961,9 @@ __device__ void no_prefix(const AttnArgs& a) {
     }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ AttnArgs a) {
-    using L = Smem<D>;
+    using L = Smem<D, TWO>;
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
@@ -969,14 +979,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     if (warp == 2) tmem_alloc(base + L::kMisc, kTmemCols);
     if (tid < L::kNumBars) {
         const int i = tid;
-        int n = 1;
-        if ((i >= L::kConvB && i < L::kConvB + L::kSlots) || (i >= L::kPFull && i < L::kPFull + 4) ||
-            i == L::kCvt || i == L::kCvt + 1)
-            n = 128;
-        if (i >= L::kScFull && i < L::kScFull + L::kScales) n = 32;
-        if (i >= L::kSegEmpty && i < L::kSegEmpty + L::kSegs) n = 19;   // the warps that read it
-        if (i >= L::kEmptyB && i < L::kEmptyB + L::kSlots && (i - L::kEmptyB) % 2 == 0) n = 2;
-        if (i == L::kXch || i == L::kEpi || (i >= L::kScFree && i < L::kScFree + L::kScales)) n = 256;
+        auto among = [&](int at, int count) { return i >= at && i < at + count; };
+        int n = 1;                                                    // arrivals of a phase
+        if (among(L::kConvB, L::kSlots) || among(L::kPFull, 4) || among(L::kCvt, 2)) n = 4;   // the warps of a group
+        if (among(L::kXch, 1) || among(L::kEpi, 1) || among(L::kScFree, L::kScales)) n = 8;     // of two
+        if (among(L::kScFull, L::kScales)) n = 32;
+        if (among(L::kSegEmpty, L::kSegs)) n = 19;                    // the warps that read it
+        if (among(L::kEmptyB, L::kSlots) && (i - L::kEmptyB) % 2 == 0) n = 2;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -996,35 +1005,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
-    // Registers go to the softmax warpgroups: 80 + 2 x 72 + 2 x 128 = the 5 x 96 at launch.  Bounded
+    // Registers go to the softmax warpgroups: 80 + 2 x 56 + 2 x 144 = the 5 x 96 at launch.  Bounded
     // waits start when the previous kernel has finished.
     if (warp < 4) {
         set_regs<80, false>();
         if (warp == 0) {
             if (!a.p.early_start) pdl_wait();
             const Sched sched = find_run(a);
-            produce<D>(a, cx, smem, base, sched);
+            produce<D, TWO>(a, cx, smem, base, sched);
         } else if (warp == 3) {
             pdl_wait();   // the workspace is the previous call's until it has finished
-            load_scales<D>(a, cx, smem);
+            load_scales<D, TWO>(a, cx, smem);
             no_prefix(a);
         } else if (warp == 1) {
             pdl_wait();
-            multiply_qk<D>(cx, smem, base, uniform(tmem));
-            drain<D>(cx, 0);
+            multiply_qk<D, TWO>(cx, smem, base, uniform(tmem));
+            drain<D, TWO>(cx, 0);
         } else if (warp == 2) {
             pdl_wait();
-            multiply_pv<D>(cx, smem, base, uniform(tmem));
-            drain<D>(cx, 1);
+            multiply_pv<D, TWO>(cx, smem, base, uniform(tmem));
+            drain<D, TWO>(cx, 1);
         }
     } else if (warp < 12) {
-        set_regs<128, true>();
+        set_regs<144, true>();
         pdl_wait();
-        softmax<D>(a, cx, smem, tmem, (warp - 4) >> 2);
+        softmax<D, TWO>(a, cx, smem, tmem, (warp - 4) >> 2);
     } else {
-        set_regs<72, false>();
+        set_regs<56, false>();
         pdl_wait();
-        convert<D, FMT>(cx, smem, tid & 127, (warp - 12) >> 2);
+        convert<D, FMT, TWO>(cx, smem, tid & 127, (warp - 12) >> 2);
     }
     __syncwarp();
     fence_before();
@@ -1220,7 +1229,7 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     a.div_hkv = divisor(d.hkv);
     a.div_unit = divisor(per_unit);
     a.div_ctas = divisor(ctas);
-    static unsigned char done[4][64], done_join[4][64];
+    static unsigned char done[8][64], done_join[8][64];
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1243,13 +1252,22 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
         lc.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&lc, join, a);
     };
-    if (d.D == 128)
-        e = d.fmt == ARKV_FMT_E5M2
-                ? go(prefix_attn_kernel<128, ARKV_FMT_E5M2>, prefix_join_kernel<128>, 0, Smem<128>::kBytes)
-                : go(prefix_attn_kernel<128, ARKV_FMT_E4M3>, prefix_join_kernel<128>, 1, Smem<128>::kBytes);
-    else
-        e = d.fmt == ARKV_FMT_E5M2 ? go(prefix_attn_kernel<64, ARKV_FMT_E5M2>, prefix_join_kernel<64>, 2, Smem<64>::kBytes)
-                                   : go(prefix_attn_kernel<64, ARKV_FMT_E4M3>, prefix_join_kernel<64>, 3, Smem<64>::kBytes);
+    auto pick = [&](auto dim, auto fmt, auto two, int which) {
+        constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
+        constexpr bool T = decltype(two)::value;
+        return go(prefix_attn_kernel<D, F, T>, prefix_join_kernel<D>, which, Smem<D, T>::kBytes);
+    };
+    using std::integral_constant;
+    auto with = [&](auto dim, auto fmt, int which) {
+        return w.row_tiles == 2 ? pick(dim, fmt, std::true_type{}, which + 4) : pick(dim, fmt, std::false_type{}, which);
+    };
+    const integral_constant<int, 128> d128{};
+    const integral_constant<int, 64> d64{};
+    const integral_constant<int, ARKV_FMT_E4M3> e4m3{};
+    const integral_constant<int, ARKV_FMT_E5M2> e5m2{};
+    const bool e5 = d.fmt == ARKV_FMT_E5M2;
+    if (d.D == 128) e = e5 ? with(d128, e5m2, 0) : with(d128, e4m3, 1);
+    else e = e5 ? with(d64, e5m2, 2) : with(d64, e4m3, 3);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
