@@ -1015,8 +1015,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             produce<D, TWO>(a, cx, smem, base, sched);
         } else if (warp == 3) {
             pdl_wait();   // the workspace is the previous call's until it has finished
+            no_prefix(a);   // while the first segment is on its way (at the end the CTA waits for it)
             load_scales<D, TWO>(a, cx, smem);
-            no_prefix(a);
         } else if (warp == 1) {
             pdl_wait();
             multiply_qk<D, TWO>(cx, smem, base, uniform(tmem));
