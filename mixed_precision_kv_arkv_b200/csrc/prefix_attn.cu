@@ -990,6 +990,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    // Rows of the query tiles that no copy fills (groups of 3: 126 and 127) are zero: their logits
+    // would move references and have jobs run again (27.7 us against 22.4 for 5 prefixes of 3900
+    // tokens, 4 key heads, 23 branches).
+    for (int i = tid; i < (TWO ? 2 : 1) * (D / 64) * 128 / 16 * (kRows - a.per_tile * a.p.d.G); i += kThreads) {
+        const int n = 8 * (kRows - a.per_tile * a.p.d.G);   // 16-byte pieces of 64 dimensions' rows
+        *reinterpret_cast<uint4*>(smem + L::kQ + (i / n + 1) * (kRows * 128) - (i % n + 1) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async();
     if (warp == 3 && lane == 0) {
         misc[1] = 0;
         prefetch_map(&a.tm_q); prefetch_map(&a.tm_k16); prefetch_map(&a.tm_v16); prefetch_map(&a.tm_k8);
