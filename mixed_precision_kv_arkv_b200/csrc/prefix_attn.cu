@@ -98,7 +98,7 @@ struct Smem {
     // reader that sees every one of its phases, whichever kinds of tile come in between.
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
                          kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4,
-                         kScFull = kPFull + 4, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
+                         kScFree = kPFull + 4, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
                          kFin = kEpi + 1, kCvt = kFin + 2, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
                          kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
@@ -306,6 +306,7 @@ __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uin
                     mma_ss(to, qd + (uint64_t)((k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2),
                            k_desc + (uint64_t)((k >> 2) * (L::kRegion >> 4) + (k & 3) * 2), kIdQK, k > 0);
                 commit(cx.bar(L::kSFull + (x & 3)));
+                if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
                 if (x + 1 == jobs) commit(cx.bar(L::kQEmpty));
             }
             __syncwarp();
@@ -320,6 +321,8 @@ __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uin
     constexpr uint32_t kIdPV = idesc_bf16(kRows, D, true);
     int j = 0;                     // tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
+    int f = 0;                     // FP8 tiles so far
+    bool fp8 = false;
     uint32_t p_ph = 0;             // parity of the next P of each of the four S
     const bool leader = elect_one();
     Seg w{};
@@ -333,6 +336,8 @@ __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uin
             if (!two || b == 0) {
                 const Tile t = tiles.next();
                 const bool c = t.fp8 || t.valid < kTok;
+                fp8 = t.fp8;
+                f += fp8;
                 if (!cx.warp_wait((c ? L::kConvB : L::kFullB) + s, ((c ? conv : full) >> s) & 1u)) return;
                 if (c) conv ^= 1u << s;
                 else full ^= 1u << s;
@@ -348,6 +353,7 @@ __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uin
                 for (int k = 0; k < kTok / 16; ++k)
                     mma_ts(to, from + 8 * k, v_desc + (uint64_t)(k * 128), kIdPV, add || k > 0);
                 if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
+                if (fp8 && (!two || b == 1)) commit(cx.bar(L::kScFree + (f - 1) % L::kScales));
                 if (x + 1 == jobs) commit(cx.bar(L::kOFull));
             }
             __syncwarp();
@@ -368,14 +374,16 @@ __device__ __forceinline__ void drain(const Ctx& cx, int which) {
 
 // ------------------------------------------------------------------ FP8 scales (one warp)
 // The K and V scales of every FP8 tile, by asynchronous copies up to kScales tiles ahead of the
-// softmax (which waits a latency of HBM for them otherwise).  Past the end of the row the last
+// softmax (which waits a latency of HBM for them otherwise).  They count among the arrivals that
+// let S = Q K^T of the tile begin, and the completion of its P V frees their place: a wait that
+// need not wait costs a softmax warp 0.13 us all the same (47.7 us against 49.8, see softmax_job).  Past the end of the row the last
 // token's: what P = 0 meets has to be finite.
 template <int D, bool TWO>
 __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
     using L = Smem<D, TWO>;
     const int lane = threadIdx.x & 31;
     const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
-    int f = 0;   // FP8 tiles so far
+    int f = 0, j = 0;   // FP8 tiles, tiles so far
     Seg w{};
     for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
@@ -388,13 +396,14 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
             const int z = f % L::kScales, use = f / L::kScales;
             if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // its last readers
 #pragma unroll
-            for (int i = 0; i < 2 * kTok; i += 32) {
-                const int tok = min(t.idx * kTok + (i & (kTok - 1)) + lane, w.n8 - 1);
-                cp_async4(to + 4 * (2 * z * kTok + i), (i < kTok ? sk : sv) + tok);
+            for (int c = 0; c < 2 * kTok; c += 32) {
+                const int tok = min(t.idx * kTok + (c & (kTok - 1)) + lane, w.n8 - 1);
+                cp_async4(to + 4 * (2 * z * kTok + c), (c < kTok ? sk : sv) + tok);
             }
-            cp_async_arrive(cx.bar(L::kScFull + z));
+            cp_async_arrive(cx.bar(L::kConvB + 2 * (j + i) % L::kSlots));
             ++f;
         }
+        j += tiles.n;
     }
     cp_async_wait_all();
 }
@@ -425,7 +434,8 @@ __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
                 // D / 2 codes a thread.  A 128-byte row's codes lie where its lower half goes: both
                 // threads of the row (one warp) read before either writes; rows of 64 codes grow
                 // over other rows' codes, so all threads do.  The upper half goes through its
-                // 16-byte chunks in another order, which keeps the two halves' banks apart.
+                // 16-byte chunks in another order, which keeps the two halves' banks apart.  (The
+                // loop is short code, see softmax_job.)
                 constexpr int N = D / 32;
                 uint4 raw[N];
 #pragma unroll
@@ -441,16 +451,21 @@ __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
                     __syncwarp();
                 }
                 char* reg = slot + (D == 128 ? h * L::kRegion : 0);
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
+                auto put = [&](const uint4& w, int c) {
                     uint4 lo, hi;
-                    fp8x4_to_bf16<FMT>(raw[c].x, lo.x, lo.y);
-                    fp8x4_to_bf16<FMT>(raw[c].y, lo.z, lo.w);
-                    fp8x4_to_bf16<FMT>(raw[c].z, hi.x, hi.y);
-                    fp8x4_to_bf16<FMT>(raw[c].w, hi.z, hi.w);
+                    fp8x4_to_bf16<FMT>(w.x, lo.x, lo.y);
+                    fp8x4_to_bf16<FMT>(w.y, lo.z, lo.w);
+                    fp8x4_to_bf16<FMT>(w.z, hi.x, hi.y);
+                    fp8x4_to_bf16<FMT>(w.w, hi.z, hi.w);
                     const int to = D == 128 ? 2 * (c ^ (2 * h)) : 4 * h + 2 * c;
                     *reinterpret_cast<uint4*>(reg + sw128(row, to)) = lo;
                     *reinterpret_cast<uint4*>(reg + sw128(row, to + 1)) = hi;
+                };
+#pragma unroll 1
+                for (int c = 0; c < N; ++c) {
+                    put(raw[0], c);
+#pragma unroll
+                    for (int i = 0; i + 1 < N; ++i) raw[i] = raw[i + 1];
                 }
             } else if (zero) {
 #pragma unroll 1
@@ -476,6 +491,11 @@ struct Rows {
     float m[4], top[4], l[4];
 };
 
+__device__ __forceinline__ void swap2(float& x, float& y) {
+    const float t = x;
+    x = y;
+    y = t;
+}
 // Over the four lanes of a row.
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
@@ -509,102 +529,114 @@ __device__ __noinline__ void rescale(uint32_t o, float ff) {
     wait_st();
 }
 
-// One job: S at column s of the warp's lanes becomes P.  The whole tile is one piece of code
-// (the exponentials set its pace, and everything else has to fit between them), which is run
-// again when the reference turns out wrong: too low, or, in a segment's first job, which starts
-// from zero, too high.  O (column o) then has to be idle: the product of the job before has
-// completed when it frees its V, entry pv.  False if that took too long.
+// One job: S at column s of the warp's lanes becomes P, 16 rows at a time by one piece of code
+// (32 rows at once are twice the instructions, which with the conversion's do not fit the cache
+// nearest to the schedulers: 51.6 us against 49.8 for a 42601-token prefix and 32 branches).
+// A half is run again when its reference turns out wrong: too low, or, in a segment's first
+// job, which starts from zero, too high.  O (column o) then has to be idle: the product of the
+// job before has completed when it frees its V, entry pv.  False if that took too long.
 template <int D, bool FP8, bool TWO>
 __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, uint32_t o, bool first, int valid,
                                             const float* sk, const float* sv, float c2, Rows& r) {
     const float2 cc = make_float2(c2, c2);
     const int col = 2 * (threadIdx.x & 3);
-    bool begin = first;
-    for (;;) {
-        // row k of the lane, columns 8 g + col and the next: va[4 g + 2 (k & 1) ..] (k < 2), vb
-        float va[32], vb[32];
-        tmem_ld_16x256b_x8(s, va);
-        tmem_ld_16x256b_x8(s + (16u << 16), vb);
-        wait_ld(va, vb);
-        if (FP8) {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        bool begin = first;
+        for (;;) {
+            // row k of the half, columns 8 g + col and the next: va[4 g + 2 k ..]
+            float va[32];
+            tmem_ld_16x256b_x8(s + half * (16u << 16), va);
+            wait_ld(va);
+            if (FP8) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const float2 ks = *reinterpret_cast<const float2*>(sk + 8 * g + col);
+                for (int g = 0; g < 8; ++g) {
+                    const float2 ks = *reinterpret_cast<const float2*>(sk + 8 * g + col);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float* v = (k < 2 ? va : vb) + 4 * g + 2 * (k & 1);
-                    const float2 x = mul2(make_float2(v[0], v[1]), ks);
-                    v[0] = x.x;
-                    v[1] = x.y;
+                    for (int k = 0; k < 2; ++k) {
+                        float* v = va + 4 * g + 2 * k;
+                        const float2 x = mul2(make_float2(v[0], v[1]), ks);
+                        v[0] = x.x;
+                        v[1] = x.y;
+                    }
                 }
             }
-        }
-        if (valid < kTok) {   // columns that are no tokens
+            if (valid < kTok) {   // columns that are no tokens
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (8 * (i / 4) + col + (i & 1) >= valid) va[i] = vb[i] = kNegInf;
-        }
-        float mx[4];
-        float2 l[4];
-        uint32_t pa[16], pb[16];   // P of rows 0, 1 and 2, 3: [2 g + row % 2]
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mx[k] = kNegInf;
-            l[k] = make_float2(0.f, 0.f);
-        }
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            float2 vs = make_float2(1.f, 1.f);
-            if (FP8) vs = *reinterpret_cast<const float2*>(sv + 8 * g + col);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float* v = (k < 2 ? va : vb) + 4 * g + 2 * (k & 1);
-                const float2 x = make_float2(v[0], v[1]);
-                mx[k] = fmaxf(fmaxf(mx[k], x.x), x.y);
-                const float2 m2 = make_float2(-r.m[k], -r.m[k]);
-                float2 p = fma2(x, cc, m2);
-                p = make_float2(ex2(p.x), ex2(p.y));
-                l[k] = add2(l[k], p);
-                if (FP8) p = mul2(p, vs);
-                (k < 2 ? pa : pb)[2 * g + (k & 1)] = pack_bf16(p.x, p.y);
+                for (int i = 0; i < 32; ++i)
+                    if (8 * (i / 4) + col + (i & 1) >= valid) va[i] = kNegInf;
             }
-        }
-        bool move = false, low = false;
+            float mx[2];
+            float2 l[2];
+            uint32_t pa[16];   // P of the two rows: [2 g + k]
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mx[k] *= c2;
-            r.top[k] = fmaxf(r.top[k], mx[k]);
-            move |= mx[k] > r.m[k] + 32.f;
-            if (begin) low |= quad_max(mx[k]) < -32.f;
-        }
-        if (!__any_sync(kFull, move || low)) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r.l[k] += l[k].x + l[k].y;
-            tmem_st_16x128b_x8(s, pa);   // over S, which has been read
-            tmem_st_16x128b_x8(s + (16u << 16), pb);
-            wait_st();
-            return true;
-        }
-        float f[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float t = quad_max(mx[k]);
-            if (begin) {
-                r.m[k] = t != kNegInf && fabsf(t) > 32.f ? t : 0.f;   // (each row for itself)
-            } else {
-                const float up = fmaxf(ceilf(t - r.m[k]), 0.f);
-                f[k] = ex2(-up);
-                r.m[k] += up;
-                r.l[k] *= f[k];
+            for (int k = 0; k < 2; ++k) {
+                mx[k] = kNegInf;
+                l[k] = make_float2(0.f, 0.f);
             }
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                float2 vs = make_float2(1.f, 1.f);
+                if (FP8) vs = *reinterpret_cast<const float2*>(sv + 8 * g + col);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float* v = va + 4 * g + 2 * k;
+                    const float2 x = make_float2(v[0], v[1]);
+                    mx[k] = fmaxf(fmaxf(mx[k], x.x), x.y);
+                    const float2 m2 = make_float2(-r.m[k], -r.m[k]);
+                    float2 p = fma2(x, cc, m2);
+                    p = make_float2(ex2(p.x), ex2(p.y));
+                    l[k] = add2(l[k], p);
+                    if (FP8) p = mul2(p, vs);
+                    pa[2 * g + k] = pack_bf16(p.x, p.y);
+                }
+            }
+            bool move = false, low = false;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mx[k] *= c2;
+                r.top[k] = fmaxf(r.top[k], mx[k]);
+                move |= mx[k] > r.m[k] + 32.f;
+                if (begin) low |= quad_max(mx[k]) < -32.f;
+            }
+            if (!__any_sync(kFull, move || low)) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) r.l[k] += l[k].x + l[k].y;
+                tmem_st_16x128b_x8(s + half * (16u << 16), pa);   // over S, which has been read
+                break;
+            }
+            float f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float t = quad_max(mx[k]);
+                if (begin) {
+                    r.m[k] = t != kNegInf && fabsf(t) > 32.f ? t : 0.f;   // (each row for itself)
+                } else {
+                    const float up = fmaxf(ceilf(t - r.m[k]), 0.f);
+                    f[k] = ex2(-up);
+                    r.m[k] += up;
+                    r.l[k] *= f[k];
+                }
+            }
+            if (!begin) {
+                if (!cx.warp_wait(Smem<D, TWO>::kEmptyB + pv % Smem<D, TWO>::kSlots, (pv / Smem<D, TWO>::kSlots) & 1)) return false;
+                fence_after();
+                const int lane = threadIdx.x & 31, src = 4 * (lane & 7);
+                const float f0 = __shfl_sync(kFull, f[0], src), f1 = __shfl_sync(kFull, f[1], src);
+                rescale<D>(o, lane >> 4 == half ? (lane & 8 ? f1 : f0) : 1.f);
+            }
+            begin = false;
         }
-        if (!begin) {
-            if (!cx.warp_wait(Smem<D, TWO>::kEmptyB + pv % Smem<D, TWO>::kSlots, (pv / Smem<D, TWO>::kSlots) & 1)) return false;
-            fence_after();
-            rescale<D>(o, row_value(f));
+        // the other half's turn
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            swap2(r.m[k], r.m[k + 2]);
+            swap2(r.top[k], r.top[k + 2]);
+            swap2(r.l[k], r.l[k + 2]);
         }
-        begin = false;
     }
+    wait_st();
+    return true;
 }
 
 template <int D, bool TWO>
@@ -634,17 +666,15 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
 #pragma unroll 1
         for (int x = 0; x < n; ++x) {
             const Tile t = tiles.next();
-            const int z = f % L::kScales, use = (f / L::kScales) & 1;
+            const int z = f % L::kScales;
             f += t.fp8;
             if (!two && (x & 1) != b) continue;
             const int buf = (two ? x : x >> 1) & 1;
             if (!cx.warp_wait(L::kSFull + b + 2 * buf, (s_ph >> buf) & 1u)) return;
             s_ph ^= 1u << buf;
             fence_after();
-            if ((threadIdx.x & 127) == 0) mbar_arrive_n(cx.bar(L::kEmptyB + 2 * (j + x) % L::kSlots), two ? 1 : 2);   // K is read
             const int pv = 2 * (j + x - (two ? 1 : 2)) + 1;   // the V of this warpgroup's job before
             if (t.fp8) {
-                if (!cx.warp_wait(L::kScFull + z, use)) return;   // complete: K came after the scales
                 const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
                 if (!softmax_job<D, true, TWO>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
             } else {
@@ -653,7 +683,6 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             first = false;
             fence_before();
             warp_arrive(cx.bar(L::kPFull + b + 2 * buf));
-            if (t.fp8) warp_arrive(cx.bar(L::kScFree + z), two ? 1 : 2);   // 8 in all, whoever read them
         }
         j += n;
         // The segment's partial, a lane a row from here.  With one tile of rows both warpgroups
@@ -982,10 +1011,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         auto among = [&](int at, int count) { return i >= at && i < at + count; };
         int n = 1;                                                    // arrivals of a phase
         if (among(L::kConvB, L::kSlots) || among(L::kPFull, 4) || among(L::kCvt, 2)) n = 4;   // the warps of a group
-        if (among(L::kXch, 1) || among(L::kEpi, 1) || among(L::kScFree, L::kScales)) n = 8;     // of two
-        if (among(L::kScFull, L::kScales)) n = 32;
+        if (among(L::kXch, 1) || among(L::kEpi, 1)) n = 8;     // of two
+        if (among(L::kConvB, L::kSlots) && (i - L::kConvB) % 2 == 0) n = 4 + 32;   // and the lanes that fetch its scales
         if (among(L::kSegEmpty, L::kSegs)) n = 19;                    // the warps that read it
-        if (among(L::kEmptyB, L::kSlots) && (i - L::kEmptyB) % 2 == 0) n = 2;
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
