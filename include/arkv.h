@@ -91,7 +91,7 @@ typedef struct arkv_cfg {
     int32_t cap_bf16;       /* slots per row, bf16 segment */
     int32_t cap_fp8;        /* slots per row, fp8 segment */
     int32_t quant_format;   /* ARKV_FMT_*: FP8 format of the Quantized tier */
-    int32_t early_start;    /* 0 or 1, arkv_decode_attn only: see there */
+    int32_t early_start;    /* 0 or 1, arkv_decode_attn and arkv_prefix_attn: see there */
 } arkv_cfg;
 
 /* Device buffers of one layer's packed cache (see Layout above). */
@@ -339,7 +339,9 @@ int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_c
  * The workspace holds at least arkv_prefix_workspace_bytes() bytes and needs no
  * preparation.  Launched as a programmatic dependent like arkv_decode_attn: with
  * cfg->early_start = 1 it reads the prefix cache and branch_start before the previous
- * kernel on the stream has finished. */
+ * kernel on the stream has finished.  Set it only when none of the three kernels that
+ * precede the call on the stream writes those buffers (nothing does while the prefix is
+ * shared: only the first step after it was packed or forked needs early_start = 0). */
 size_t arkv_prefix_workspace_bytes(const arkv_cfg *cfg, const arkv_cfg *prefix_cfg);
 int arkv_prefix_attn(const arkv_cfg *cfg, const arkv_cfg *prefix_cfg, const uint16_t *q,
                      const arkv_layer_cache *prefix, const int32_t *branch_start,

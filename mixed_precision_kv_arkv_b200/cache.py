@@ -103,6 +103,8 @@ def decode_step(st: LayerState, step: int, q, k_new, v_new, ctx_len, o, reassign
 
 def _on_device(t: torch.Tensor, stream):
     """The device guard and raw stream of a call on t's device."""
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
     s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
     return torch.cuda.device(t.device), s
 
@@ -170,8 +172,11 @@ def new_shared_prefix(branches: abi.arkv_cfg, cache: LayerCache, branch_start=No
         branch_start = torch.as_tensor(branch_start, dtype=torch.int32, device=dev).contiguous()
         if branch_start.numel() != cache.cfg.batch + 1:
             raise ValueError("branch_start must have one entry per prefix and one more")
-    return SharedPrefix(cache, branch_start,
-                        Workspace(abi.arkv_prefix_workspace_bytes(branches, cache.cfg), dev))
+    nbytes = abi.arkv_prefix_workspace_bytes(branches, cache.cfg)
+    if nbytes == 0:
+        raise ValueError("the branches and the prefixes do not fit together: "
+                         + abi.lib().arkv_last_error_string().decode())
+    return SharedPrefix(cache, branch_start, Workspace(nbytes, dev))
 
 
 def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new, ctx_len, o_own, o,
@@ -180,6 +185,10 @@ def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new
     tokens (o_own, float32), attend to the prefix and join (o, bf16, and the heads' (max, sum) in
     the decode workspace), score update of the own tokens, and their reassignment when
     (step + 1) % reassign_interval == 0.  ctx_len counts the prefix's tokens."""
+    for name, t, dt in (("q", q, torch.bfloat16), ("k_new", k_new, torch.bfloat16), ("v_new", v_new, torch.bfloat16),
+                        ("ctx_len", ctx_len, torch.int32), ("o_own", o_own, torch.float32), ("o", o, torch.bfloat16)):
+        if t.dtype != dt or t.device != q.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dt} on {q.device}")
     guard, s = _on_device(q, stream)
     with guard:
         abi.arkv_decode_attn(st.cfg, step, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), ctx_len.data_ptr(),

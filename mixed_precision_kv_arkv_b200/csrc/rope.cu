@@ -112,13 +112,16 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     wo[2 * e] = bf16_lo(aw[e]); wo[2 * e + 1] = bf16_hi(aw[e]);
-                    wp[2 * e] = bf16_lo(qw[e]); wp[2 * e + 1] = bf16_hi(qw[e]);
+                    if (rotated) {   // (else the factor of no partner has to be zero, whatever the weight)
+                        wp[2 * e] = bf16_lo(qw[e]);
+                        wp[2 * e + 1] = bf16_hi(qw[e]);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     wo[e] = bf16_to_f32(w[dim0 + e]);
-                    wp[e] = bf16_to_f32(w[partner_dim(dim0 + e)]);
+                    if (dim0 + e < p.rot) wp[e] = bf16_to_f32(w[partner_dim(dim0 + e)]);
                 }
             }
         }

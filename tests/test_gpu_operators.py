@@ -416,3 +416,123 @@ def test_shared_and_forked_prompts_decode_alike(cuda, fmt, d, early):
     C.branch_step(shared, sp, steps, q, kn, vn, bctx, o_own, o, 1)       # with a reassignment
     torch.cuda.synchronize()
     assert torch.isfinite(o).all() and int(a.status) == 0 and int(prompt.status) == 0
+
+
+# ------------------------------------------------------------------ corners
+@pytest.mark.parametrize("d,rot,inter", [(128, 64, 0), (64, 50, 0), (128, 64, 1), (64, 0, 0)])
+def test_qk_norm_rope_infinite_weight_stays_in_its_dimension(cuda, d, rot, inter):
+    """An infinite weight of a dimension that is not rotated reaches that dimension alone."""
+    c = R.cfg(2, 4, 1, d)
+    qkv = torch.randn((2, 6 * d), generator=gen(cuda, 40), device=cuda).bfloat16()
+    w = (1 + 0.1 * torch.randn(d, generator=gen(cuda, 41), device=cuda)).bfloat16()
+    freq = C.rope_frequencies(rot, 1e4, cuda) if rot else None
+    mk = lambda h: torch.empty((2, h, 1, d), dtype=torch.bfloat16, device=cuda)
+    outs = []
+    for last in (1.0, float("inf")):
+        w[d - 3] = last
+        q, k, v = mk(4), mk(1), mk(1)
+        C.qk_norm_rope(c, qkv, 1, freq, k, v, q, q_weight=w, k_weight=w, interleaved=inter, step=5)
+        outs.append(torch.cat([q, k], 1))
+    others = [i for i in range(d) if i != d - 3]
+    assert torch.equal(outs[0][..., others], outs[1][..., others])
+    assert torch.isinf(outs[1][..., d - 3]).all()
+
+
+def test_prefix_attn_of_empty_prefixes(cuda):
+    """No prefix token anywhere: the own part comes through (one rounding to bf16), or zeros."""
+    pc, c = R.cfg(2, 8, 2, 128, 20, 20), R.cfg(5, 8, 2, 128)
+    prefix = R.random_cache(pc, [0, 0], [0, 0], cuda, 42)
+    q = torch.randn((5, 8, 128), generator=gen(cuda, 43), device=cuda).bfloat16()
+    o_own, ml_own = own_part(c, cuda, 44, 3.0)
+    o, ml = run_prefix(c, prefix, q, [0, 2, 5], o_own, ml_own)
+    R.check_prefix(c, o, ml, R.prefix_attn(c, prefix, q, [0, 2, 5], o_own, ml_own))
+    o, ml = run_prefix(c, prefix, q, [0, 2, 5])
+    assert (o == 0).all() and (ml[..., 0] == float("-inf")).all() and (ml[..., 1] == 0).all()
+
+
+@pytest.mark.parametrize("d,branches", [(64, 3), (128, 3), (128, 40)])
+def test_prefix_attn_zero_scales(cuda, d, branches):
+    """K and V scales of zero, the last live token's among them (its scale is what the columns
+    past the end of a tile meet)."""
+    prefix = R.random_cache(R.cfg(1, 8, 2, d, 70, 170), [70], [157], cuda, 45)
+    prefix.sk[:, [3, 80, 156]] = 0.0
+    prefix.sv[:, [4, 81, 156]] = 0.0
+    c = R.cfg(branches, 8, 2, d)
+    q = torch.randn((branches, 8, d), generator=gen(cuda, 46), device=cuda).bfloat16()
+    o, ml = run_prefix(c, prefix, q, None)
+    R.check_prefix(c, o, ml, R.prefix_attn(c, prefix, q, [0, branches]))
+
+
+def test_rows_past_31_bits(cuda):
+    """A cache whose rows lie past 2^31 elements and bytes: forked in place, shared and read."""
+    cap = 2200001
+    cache = R.random_cache(R.cfg(2, 8, 4, 128, cap, cap + 7), [300, 5], [257, 9], cuda, 47)
+    assert cache.k8.numel() > 2 ** 31 and cache.k16.numel() > 2 ** 31
+    C.fork(cache, cache, torch.tensor([0, 0], dtype=torch.int32, device=cuda))
+    small = C.LayerCache(R.cfg(1, 8, 4, 128, 400, 400), cuda)
+    C.fork(small, cache, torch.tensor([1], dtype=torch.int32, device=cuda))
+    for f, n in [(f, 300) for f in R.FIELDS16] + [(f, 257) for f in R.FIELDS8]:
+        x = getattr(cache, f)
+        assert torch.equal(bits(x[:4, :n]), bits(x[4:, :n])) and torch.equal(bits(x[4:, :n]), bits(getattr(small, f)[:, :n])), f
+    c = R.cfg(5, 8, 4, 128)
+    q = torch.randn((5, 8, 128), generator=gen(cuda, 48), device=cuda).bfloat16()
+    o, ml = run_prefix(c, cache, q, [0, 2, 5])
+    R.check_prefix(c, o, ml, R.prefix_attn(c, cache, q, [0, 2, 5]))
+
+
+def test_calls_on_two_streams_at_once(cuda):
+    """Calls on two streams, each with its workspace, and several on one workspace one after the
+    other: the bits of calls made alone."""
+    c, pc = R.cfg(36, 8, 2, 128), R.cfg(2, 8, 2, 128, 2000, 1500)
+    prefix = R.random_cache(pc, [2000, 900], [1500, 1100], cuda, 49)
+    starts = [0, 20, 36]
+    qs = [torch.randn((36, 8, 128), generator=gen(cuda, 50 + i), device=cuda).bfloat16() for i in range(6)]
+    alone = []
+    for q in qs:
+        alone.append(run_prefix(c, prefix, q, starts))
+        torch.cuda.synchronize()
+    sides = [(torch.cuda.Stream(), C.new_shared_prefix(c, prefix, starts)) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i, q in enumerate(qs):
+        with torch.cuda.stream(sides[i % 2][0]):
+            got.append(run_prefix(c, prefix, q, starts, sp=sides[i % 2][1]))
+    torch.cuda.synchronize()
+    for a, b in zip(got, alone):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert int(prefix.status) == 0
+
+
+def test_many_small_prefixes(cuda):
+    """More rows than a warp has lanes, most without branches or tokens."""
+    P, hkv = 100, 4
+    n16, n8 = [(i % 7 == 0) * (i + 1) for i in range(P)], [(i % 5 == 0) * 2 * i for i in range(P)]
+    sizes = [(i % 3 == 0) * (1 + i % 4) for i in range(P)]
+    starts = [0]
+    for s in sizes:
+        starts.append(starts[-1] + s)
+    prefix = R.random_cache(R.cfg(P, 8, hkv, 64, 110, 210, fmt="e5m2"), n16, n8, cuda, 56)
+    c = R.cfg(starts[-1], 8, hkv, 64)
+    q = torch.randn((c.batch, 8, 64), generator=gen(cuda, 57), device=cuda).bfloat16()
+    o_own, ml_own = own_part(c, cuda, 58, 1.0)
+    o, ml = run_prefix(c, prefix, q, starts, o_own, ml_own)
+    R.check_prefix(c, o, ml, R.prefix_attn(c, prefix, q, starts, o_own, ml_own))
+
+
+def test_wrapper_refusals(cuda):
+    prompt = C.LayerCache(R.cfg(1, 8, 2, 64, 10, 10), cuda)
+    c = C.make_cfg(2, 8, 2, 64, 4, 4, 1.0, 0.5, 20, 20, "e4m3")
+    with pytest.raises(ValueError):
+        C.new_shared_prefix(C.make_cfg(2, 8, 2, 128, 4, 4, 1.0, 0.5, 20, 20, "e4m3"), prompt)
+    with pytest.raises(ValueError):
+        C.new_shared_prefix(c, prompt, [0, 1, 2])
+    st, sp = C.new_layer_state(c, 0.5, cuda), C.new_shared_prefix(c, prompt)
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device=cuda)
+    a = dict(q=z(2, 8, 1, 64), k_new=z(2, 2, 1, 64), v_new=z(2, 2, 1, 64), ctx_len=z(2, dt=torch.int32),
+             o_own=z(2, 8, 64, dt=torch.float32), o=z(2, 8, 64))
+    for bad in (dict(o=a["o_own"]), dict(o_own=a["o"]), dict(q=a["o_own"]), dict(ctx_len=z(2, dt=torch.int64)),
+                dict(k_new=z(2, 2, 64, 2).transpose(2, 3)[:, :, :1])):
+        with pytest.raises(ValueError):
+            C.branch_step(st, sp, 0, **{**a, **bad}, reassign_interval=100)
+    with pytest.raises(ValueError):
+        C.fork(st.cache, prompt, torch.zeros(2, device=cuda))

@@ -84,3 +84,15 @@ def test_decode_ml_is_inside_the_workspace():
     out = ctypes.c_void_p()
     assert abi.lib().arkv_decode_ml(ctypes.byref(c), P, need - 1, ctypes.byref(out)) == abi.ARKV_EINVAL
     assert abi.lib().arkv_decode_ml(ctypes.byref(c), P, need, None) == abi.ARKV_EINVAL
+
+
+def test_wrappers_refuse_tensors_of_the_host():
+    import torch
+    from mixed_precision_kv_arkv_b200 import cache as C
+    c = cfg(batch=1, hq=2, hkv=1)
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        C.qk_norm_rope(c, z(1, 256), 1, None, z(1, 1, 1, 64), z(1, 1, 1, 64))
+    small = C.LayerCache(cfg(batch=1, cap_bf16=4, cap_fp8=4), "cpu")
+    with pytest.raises(ValueError):
+        C.fork(small, small, torch.zeros(1, dtype=torch.int32))
