@@ -13,7 +13,7 @@
 // position * round(freq / 2 pi * 2^64) modulo 2^64, is exact for any position.
 //
 // Bound: HBM, every projection row read and every output written once.  8192 tokens of 48
-// heads of 128: 201.9 MB, floor 31.2 us at 6461.5 GB/s; 43.9 us measured (4.6 TB/s; the
+// heads of 128: 201.9 MB, floor 31.2 us at 6461.5 GB/s; 42.5 us measured (4.8 TB/s; the
 // loads' and shuffles' latencies at 32 warps an SM and half of the issue slots are what is left).
 #include "arkv_internal.cuh"
 #include "tc.cuh"
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
     const int lt = group / per, row = row0 + lt;
     const int stride = per * gridDim.y, first = (group - lt * per) + per * blockIdx.y;
     const int b = row / p.n_tok, t = row - b * p.n_tok;   // (past the end only when not `in`)
-    const bool in = (unsigned)row < (unsigned)total;
+    const bool in = lt < tokens && (unsigned)row < (unsigned)total;
     const int len = in ? (p.length ? min(max(p.length[b], 0), p.n_tok) : p.n_tok) : 0;
     if (!in || t >= len) return;           // whole groups; the shuffles stay within a group
     const unsigned mask = (kGroup == 32 ? 0xffffffffu : ((1u << kGroup) - 1u) << ((tid & 31) / kGroup * kGroup));
@@ -234,9 +234,15 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s) {
     // tokens as leave a group 48 heads, or two blocks an SM (8192 tokens of 48 heads: 2 tokens a
     // block 67 us, 4 54, 8 45, 16 44; 6964 of 12 heads of 64: 4 tokens 15, 16 10.8).  A call of
     // few tokens gives each a block, or several (at most a head a group), up to two an SM.
+    const int heads = d.hq + 2 * d.hkv;
     int tokens = 1;
-    while (tokens < kMaxTokens && (d.hq + 2 * d.hkv) * tokens < groups * 48 && total >= 2ll * 148 * tokens) tokens *= 2;
-    const int per = groups / tokens, heads = d.hq + 2 * d.hkv;
+    while (tokens < kMaxTokens && heads * tokens < groups * 48 && total >= 2ll * 148 * tokens) tokens *= 2;
+    // Calls of one wave (four blocks an SM) give every block the same number of tokens instead, so
+    // that no SM has a block more than another, if that leaves a group 7 heads or more (48 heads of
+    // 128: 4096 tokens 30.4 -> 23.1 us, 1500 tokens 15.7 -> 14.6, but 800 tokens 9.7 -> 10.1).
+    const long long wave = 4 * 148, even = (total + wave - 1) / wave;
+    if (even <= kMaxTokens && even * heads >= 7 * groups) tokens = (int)even;
+    const int per = groups / tokens;
     long long split = 1;
     while (tokens == 1 && total * split < 2 * 148 && split * per < heads) ++split;
     cudaLaunchConfig_t lc{};
