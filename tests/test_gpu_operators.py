@@ -47,7 +47,7 @@ ROPE_CASES = [
     (5, 130, 12, 3, 128, 16, 0, True, True, 0, 0),
     (150, 1, 8, 2, 128, 128, 0, True, False, 0, 9999),
     (3, 1001, 16, 4, 128, 128, 0, True, True, 0, 3),     # token counts a block's groups do not divide by
-    (7, 1003, 16, 4, 64, 64, 1, True, True, 0, 11),
+    (5, 1403, 16, 4, 64, 64, 1, True, True, 0, 11),
     (1, 8000, 16, 4, 64, 48, 0, True, False, 0, 0),
 ]
 
