@@ -6,30 +6,39 @@
 // once for all of them and both products run on the tensor cores:
 //   S[128 rows][64 tokens] = Q K^T,   O[128 rows][D] += P V,   P = 2^(S c - m).
 //
-// Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 64 tokens
-// are the bf16 and the FP8 tiles of the prefix row.  The tiles of all units form one list,
-// cut into equal runs, one a CTA and one CTA an SM (with shares of a unit's bf16 and FP8 tiles
-// in proportion: an FP8 tile has twice the arithmetic per byte); a run that crosses units is several segments,
-// each with a partial (max, sum, unnormalised o) in the workspace.  In the list every unit
-// begins with kSegCost empty places, about what the start of another segment costs, so
-// that the run that holds them has that many tiles less.
+// Work.  A unit is (prefix, key head, one or two tiles of rows); its tiles of 64 tokens are
+// the bf16 and the FP8 tiles of the prefix row.  The tiles of all units form one list, cut
+// into equal runs, one a CTA and one CTA an SM (with shares of a unit's bf16 and FP8 tiles in
+// proportion: an FP8 tile has twice the arithmetic per byte).  A run that crosses units is
+// several segments, each with a partial (max, sum, unnormalised o) in the workspace.  In the
+// list every unit begins with kSegCost empty places, about what the start of another segment
+// costs, so that the run that holds them has that many tiles less.
 // prefix_join_kernel joins the partials and the branch's own part.
 //
-// A CTA: warp 0 walks the run, streams K and V by TMA through a ring of slots (a slot is a
-// tile's K or its V) and hands the segments to the others through shared memory, warps
-// 1 and 2 issue the products, warp 3 fetches FP8 scales, two warpgroups do the softmax, each with its own two S (and P)
-// and O in tensor memory and its own state, so that neither waits for the other, and two
-// warpgroups rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits), one K,
-// one V.  With one tile of rows the softmax
-// warpgroups take the token tiles in turn and their two O are added at the end of the
-// segment; with two each has its rows, and a token tile is loaded and converted once for
-// both.  Either way a softmax job is one S, and the jobs alternate.
-// P takes the place of S.  The K scale of an FP8 token enters the exponent's factor, its V
-// scale is folded into P.
+// A CTA.  Warp 0 walks the run, streams K and V by TMA through a ring of slots (a slot is a
+// tile's K or its V) and hands the segments to the others through shared memory.  Warps 1 and
+// 2 issue the products, warp 3 fetches FP8 scales.  Two warpgroups do the softmax, each with
+// its own two S (and P) and O in tensor memory and its own state, so that neither waits for
+// the other.  Two more rewrite FP8 tiles in place as bf16 (exact: 4 or 3 significant bits),
+// one the K tiles, one the V tiles.  With one tile of rows the softmax warpgroups take the
+// token tiles in turn and their two O are added at the end of the segment; with two each has
+// its rows, and a token tile is loaded and converted once for both.  Either way a softmax job
+// is one S, and the jobs alternate.
+// P takes the place of S.  The K scale of an FP8 token multiplies its logit, its V scale is
+// folded into P.
 // The softmax reference m starts as zero and moves only when a logit exceeds it by 2^32 (or
-// the first tile's are all as far below: float32 and bf16 have the range), so O is hardly ever
-// rescaled and a job needs no maximum before its exponentials.  P is rounded to bf16 once, the rounding that o itself gets; the
-// sum is of the unrounded values.
+// the first tile's are all as far below: float32 and bf16 have the range), so O is hardly
+// ever rescaled and a job needs no maximum before its exponentials.  P is rounded to bf16
+// once, the rounding that o itself gets; the sum is of the unrounded values.
+//
+// Bound.  HBM for one tile of rows, the tensor cores for two (floors of a prefix of
+// 23701 bf16 and 18900 FP8 tokens, 8 key heads of 128: 21.2 us for 128 rows, 26.8 us for 256).
+// Measured with the join: 47.7 and 70.7 us; 21.7 us for 5921 + 4739 tokens and 128 rows
+// (floor 5.3).  What takes the time is the issue of the softmax and the conversion: a job of
+// 128 x 64 logits takes a warp 1.0 us (bf16) to 1.4 us (FP8) with two softmax and two
+// conversion warps on each scheduler, of which a fifth is instruction fetch.  About 12 us of
+// every call are start (4 us until the first S), end of the segment, and the join.
+//
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
 // memory is freed and the call ends.
@@ -55,7 +64,7 @@ constexpr int kTok = 64;              // tokens of a tile
 constexpr int kWarps = 20;            // 4 of single roles, 2 x 4 softmax, 2 x 4 conversion
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;         // of one call
-constexpr int kSegCost = 5;           // a segment's start and end, in tiles
+constexpr int kSegCost = 5;           // a segment's start and end, in tiles (4 to 7 measure alike, 2 is 4% slower)
 constexpr int kSpinLimit = 1 << 20;   // polls of one wait
 
 struct RowInfo {
@@ -93,12 +102,13 @@ struct Smem {
     static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K and V scales
     static constexpr int kScales = 4;
     static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
-    // mbarriers.  K is in the even slots, V in the odd ones.  A slot's load completes on kFullB, or on kRawB (K) or kRawB + kSlots (V) if
-    // the tile has to be converted first (kConvB tells when): each barrier then has one
-    // reader that sees every one of its phases, whichever kinds of tile come in between.
+    // mbarriers.  K is in the even slots, V in the odd ones.  A slot's load completes on kFullB,
+    // or on kRawB (K) or kRawB + kSlots (V) if the tile has to be converted first (kConvB tells
+    // when): each barrier then has one reader that sees every one of its phases, whichever kinds
+    // of tile come in between.
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
                          kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4,
-                         kScFree = kPFull + 4, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
+                         kScFull = kPFull + 4, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
                          kFin = kEpi + 1, kCvt = kFin + 2, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
                          kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
@@ -274,7 +284,7 @@ template <int D, bool TWO>
 __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D, TWO>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false);
-    int j = 0;                     // tiles so far
+    int j = 0, f = 0;              // tiles, FP8 tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
@@ -292,6 +302,10 @@ __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uin
                 const int ev = 2 * (j + before) + 1;
                 if (before >= 0 && !cx.warp_wait(L::kEmptyB + ev % L::kSlots, (ev / L::kSlots) & 1)) return;
                 const bool c = tiles.next().fp8;
+                if (c) {   // (the scales come before the converted K)
+                    if (!cx.warp_wait(L::kScFull + f % L::kScales, (f / L::kScales) & 1)) return;
+                    ++f;
+                }
                 if (!cx.warp_wait((c ? L::kConvB : L::kFullB) + s, ((c ? conv : full) >> s) & 1u)) return;
                 if (c) conv ^= 1u << s;
                 else full ^= 1u << s;
@@ -374,16 +388,17 @@ __device__ __forceinline__ void drain(const Ctx& cx, int which) {
 
 // ------------------------------------------------------------------ FP8 scales (one warp)
 // The K and V scales of every FP8 tile, by asynchronous copies up to kScales tiles ahead of the
-// softmax (which waits a latency of HBM for them otherwise).  They count among the arrivals that
-// let S = Q K^T of the tile begin, and the completion of its P V frees their place: a wait that
-// need not wait costs a softmax warp 0.13 us all the same (47.7 us against 49.8, see softmax_job).  Past the end of the row the last
-// token's: what P = 0 meets has to be finite.
+// softmax (which waits a latency of HBM for them otherwise).  The warp that issues S = Q K^T
+// waits for them, so that a full S tells the softmax that they are there too, and the completion
+// of the tile's P V frees their place: a wait that need not wait costs a softmax warp 0.13 us all
+// the same (47.7 us against 49.8, see softmax_job).  Past the end of the row the last token's:
+// what P = 0 meets has to be finite.
 template <int D, bool TWO>
 __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
     using L = Smem<D, TWO>;
     const int lane = threadIdx.x & 31;
     const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
-    int f = 0, j = 0;   // FP8 tiles, tiles so far
+    int f = 0;   // FP8 tiles so far
     Seg w{};
     for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
@@ -400,10 +415,9 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
                 const int tok = min(t.idx * kTok + (c & (kTok - 1)) + lane, w.n8 - 1);
                 cp_async4(to + 4 * (2 * z * kTok + c), (c < kTok ? sk : sv) + tok);
             }
-            cp_async_arrive(cx.bar(L::kConvB + 2 * (j + i) % L::kSlots));
+            cp_async_arrive(cx.bar(L::kScFull + z));
             ++f;
         }
-        j += tiles.n;
     }
     cp_async_wait_all();
 }
@@ -482,8 +496,8 @@ __device__ void convert(const Ctx& cx, char* smem, int ct, int kv) {
 // ------------------------------------------------------------------ softmax (128 threads)
 // A warp owns 32 rows (tensor-memory lanes).  S is read in the matrix layout: lane t holds of
 // rows t / 4 + 8 k (k = 0..3) the columns 2 (t % 4), 2 (t % 4) + 1 of every 8, so that the
-// per-column FP8 scales are read once for four rows (a lane a row, every lane reads every
-// scale, and the shared memory's bandwidth set the time: 3.1 us a job against 1.9).
+// per-column FP8 scales are read once for two rows (a lane a row, every lane reads every
+// scale, and the shared memory's bandwidth sets the time).
 // State of a lane's rows in log2 units (logit * log2(e) / sqrt(D)): the reference m of P
 // and O (the same in the four lanes of a row), the largest logit top and the sum l of
 // 2^(x - m), both of this lane's columns alone.
@@ -1012,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         int n = 1;                                                    // arrivals of a phase
         if (among(L::kConvB, L::kSlots) || among(L::kPFull, 4) || among(L::kCvt, 2)) n = 4;   // the warps of a group
         if (among(L::kXch, 1) || among(L::kEpi, 1)) n = 8;     // of two
-        if (among(L::kConvB, L::kSlots) && (i - L::kConvB) % 2 == 0) n = 4 + 32;   // and the lanes that fetch its scales
+        if (among(L::kScFull, L::kScales)) n = 32;
         if (among(L::kSegEmpty, L::kSegs)) n = 19;                    // the warps that read it
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
