@@ -33,7 +33,7 @@
 //
 // Bound.  HBM for one tile of rows, the tensor cores for two (floors of a prefix of
 // 23701 bf16 and 18900 FP8 tokens, 8 key heads of 128: 21.2 us for 128 rows, 26.8 us for 256).
-// Measured with the join: 47.7 and 70.7 us; 21.7 us for 5921 + 4739 tokens and 128 rows
+// Measured with the join: 48.2 and 70.8 us; 21.5 us for 5921 + 4739 tokens and 128 rows
 // (floor 5.3).  What takes the time is the issue of the softmax and the conversion: a job of
 // 128 x 64 logits takes a warp 1.0 us (bf16) to 1.4 us (FP8) with two softmax and two
 // conversion warps on each scheduler, of which a fifth is instruction fetch.  About 12 us of
@@ -100,7 +100,7 @@ struct Smem {
     static constexpr int kQTile = kRows * D * 2;
     static constexpr int kRing = (TWO ? 2 : 1) * kQTile;
     static constexpr int kScale = kRing + kSlots * kSlot;   // float [kScales][2][kTok]: K and V scales
-    static constexpr int kScales = 4;
+    static constexpr int kScales = 4;                       // tiles of scales, fewer than the ring has
     static constexpr int kBars = kScale + kScales * 2 * kTok * 4;
     // mbarriers.  K is in the even slots, V in the odd ones.  A slot's load completes on kFullB,
     // or on kRawB (K) or kRawB + kSlots (V) if the tile has to be converted first (kConvB tells
@@ -108,12 +108,13 @@ struct Smem {
     // of tile come in between.
     static constexpr int kFullB = 0, kEmptyB = kSlots, kConvB = 2 * kSlots, kRawB = 3 * kSlots, kQFull = 5 * kSlots,
                          kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kPFull = kSFull + 4,
-                         kScFull = kPFull + 4, kScFree = kScFull + kScales, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
+                         kScFree = kPFull + 4, kOFull = kScFree + kScales, kXch = kOFull + 1, kEpi = kXch + 1,
                          kFin = kEpi + 1, kCvt = kFin + 2, kSegFull = kCvt + 2, kSegEmpty = kSegFull + kSegs,
                          kNumBars = kSegEmpty + kSegs;
     static constexpr int kMisc = kBars + ((kNumBars * 8 + 15) & ~15);   // tensor-memory base, abort flag
     static constexpr int kSeg = kMisc + 16;                             // Seg [kSegs]
     static constexpr int kBytes = kSeg + kSegs * 64;
+    static_assert(kScales < kSlots / 2, "see load_scales");
     static_assert(sizeof(Seg) <= 64 && kBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -284,7 +285,7 @@ template <int D, bool TWO>
 __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D, TWO>;
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kTok, false);
-    int j = 0, f = 0;              // tiles, FP8 tiles so far
+    int j = 0;                     // tiles so far
     uint32_t full = 0, conv = 0;   // parity of each slot's next phase
     const bool leader = elect_one();
     const uint64_t q_desc = desc_sw128(smem + L::kQ, 16, 1024);
@@ -302,10 +303,6 @@ __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uin
                 const int ev = 2 * (j + before) + 1;
                 if (before >= 0 && !cx.warp_wait(L::kEmptyB + ev % L::kSlots, (ev / L::kSlots) & 1)) return;
                 const bool c = tiles.next().fp8;
-                if (c) {   // (the scales come before the converted K)
-                    if (!cx.warp_wait(L::kScFull + f % L::kScales, (f / L::kScales) & 1)) return;
-                    ++f;
-                }
                 if (!cx.warp_wait((c ? L::kConvB : L::kFullB) + s, ((c ? conv : full) >> s) & 1u)) return;
                 if (c) conv ^= 1u << s;
                 else full ^= 1u << s;
@@ -388,17 +385,16 @@ __device__ __forceinline__ void drain(const Ctx& cx, int which) {
 
 // ------------------------------------------------------------------ FP8 scales (one warp)
 // The K and V scales of every FP8 tile, by asynchronous copies up to kScales tiles ahead of the
-// softmax (which waits a latency of HBM for them otherwise).  The warp that issues S = Q K^T
-// waits for them, so that a full S tells the softmax that they are there too, and the completion
-// of the tile's P V frees their place: a wait that need not wait costs a softmax warp 0.13 us all
-// the same (47.7 us against 49.8, see softmax_job).  Past the end of the row the last token's:
-// what P = 0 meets has to be finite.
+// softmax (which waits a latency of HBM for them otherwise).  They count among the arrivals that
+// let S = Q K^T of the tile begin, and the completion of its P V frees their place: a wait that
+// need not wait costs a softmax warp 0.13 us all the same.
+// Past the end of the row the last token's: what P = 0 meets has to be finite.
 template <int D, bool TWO>
 __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
     using L = Smem<D, TWO>;
     const int lane = threadIdx.x & 31;
     const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
-    int f = 0;   // FP8 tiles so far
+    int f = 0, j = 0, last = 0;   // FP8 tiles, tiles so far; the last FP8 tile
     Seg w{};
     for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
@@ -410,14 +406,22 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
             if (!t.fp8) continue;
             const int z = f % L::kScales, use = f / L::kScales;
             if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // its last readers
+            // The slot's barrier has to be done with the FP8 tile that had the slot before.  In a run
+            // of FP8 tiles that one is more than kScales back, so the wait above shows it; after bf16
+            // tiles (of a new segment) every FP8 tile so far has to be done.
+            if (f > 0 && j + i > last + 1 &&
+                !cx.warp_wait(L::kScFree + (f - 1) % L::kScales, ((f - 1) / L::kScales) & 1))
+                return;
 #pragma unroll
             for (int c = 0; c < 2 * kTok; c += 32) {
                 const int tok = min(t.idx * kTok + (c & (kTok - 1)) + lane, w.n8 - 1);
                 cp_async4(to + 4 * (2 * z * kTok + c), (c < kTok ? sk : sv) + tok);
             }
-            cp_async_arrive(cx.bar(L::kScFull + z));
+            cp_async_arrive(cx.bar(L::kConvB + 2 * (j + i) % L::kSlots));
+            last = j + i;
             ++f;
         }
+        j += tiles.n;
     }
     cp_async_wait_all();
 }
@@ -982,7 +986,9 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
 }
 
 // Tells the join which branches have no prefix token (a CTA's share of the branches).
-__device__ void no_prefix(const AttnArgs& a) {
+// (Out of line, so that it does not lie between the loops that run all the time: 48.2 us against
+// 51.1 for a 42601-token prefix and 32 branches.)
+__device__ __noinline__ void no_prefix(const AttnArgs& a) {
     const LayerDims& d = a.p.d;
     for (int b = blockIdx.x * 32 + (threadIdx.x & 31); b < a.p.branches; b += gridDim.x * 32) {
         int pre = 0;
@@ -1026,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         int n = 1;                                                    // arrivals of a phase
         if (among(L::kConvB, L::kSlots) || among(L::kPFull, 4) || among(L::kCvt, 2)) n = 4;   // the warps of a group
         if (among(L::kXch, 1) || among(L::kEpi, 1)) n = 8;     // of two
-        if (among(L::kScFull, L::kScales)) n = 32;
+        if (among(L::kConvB, L::kSlots) && (i - L::kConvB) % 2 == 0) n = 4 + 32;   // and the lanes that fetch scales
         if (among(L::kSegEmpty, L::kSegs)) n = 19;                    // the warps that read it
         mbar_init(cx.bar(i), n);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

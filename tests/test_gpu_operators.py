@@ -522,6 +522,23 @@ def test_many_small_prefixes(cuda):
     R.check_prefix(c, o, ml, R.prefix_attn(c, prefix, q, starts, o_own, ml_own))
 
 
+@pytest.mark.parametrize("branches", [40, 1400])
+def test_prefix_attn_runs_over_many_units(cuda, branches):
+    """Runs that cross units, with every number of bf16 tiles between the FP8 tiles of one unit and
+    of the next, for one and two tiles of rows."""
+    P, hkv = 40, 2
+    n16, n8 = [64 * (i % 13) + (i % 3) for i in range(P)], [64 * ((5 * i) % 17) + 1 for i in range(P)]
+    starts = [branches * i // P for i in range(P + 1)]
+    prefix = R.random_cache(R.cfg(P, 8, hkv, 128, 800, 1100), n16, n8, cuda, 60)
+    c = R.cfg(branches, 8, hkv, 128)
+    q = torch.randn((branches, 8, 128), generator=gen(cuda, 61), device=cuda).bfloat16()
+    first, ml = run_prefix(c, prefix, q, starts)
+    R.check_prefix(c, first, ml, R.prefix_attn(c, prefix, q, starts))
+    for _ in range(20):
+        assert torch.equal(run_prefix(c, prefix, q, starts)[0], first)
+    assert int(prefix.status) == 0
+
+
 def test_wrapper_refusals(cuda):
     prompt = C.LayerCache(R.cfg(1, 8, 2, 64, 10, 10), cuda)
     c = C.make_cfg(2, 8, 2, 64, 4, 4, 1.0, 0.5, 20, 20, "e4m3")
