@@ -333,8 +333,8 @@ int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_c
  *          each group.  ml may be ml_own: with the address of arkv_decode_ml for both,
  *          the arkv_score_update that follows sees the whole softmax
  * A head without any token gets o = 0 and (M, L) = (-inf, 0).  A probability enters the
- * product with V rounded to bf16 (the rounding of o itself), or to twice as many bits where
- * the prefixes' capacities are small; sums are float32.
+ * product with V as the sum of two bf16 parts (16 bits, as in arkv_decode_attn); sums are
+ * float32.
  * The prefix is only read: its tokens are neither scored nor reassigned while it is
  * shared.  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
  * The workspace holds at least arkv_prefix_workspace_bytes() bytes and needs no

@@ -28,11 +28,10 @@
 // folded into P.
 // The softmax reference m starts as zero and moves only when a logit exceeds it by 2^32 (or
 // the first tile's are all as far below: float32 and bf16 have the range), so O is hardly
-// ever rescaled and a job needs no maximum before its exponentials.  P is rounded to bf16
-// once, the rounding that o itself gets; the sum is of the unrounded values.  FINE: P as the
-// sum of two bf16 parts, which take all of S's place (each is multiplied with V: two products
-// more a tile, and more instructions a job), for short lists of tiles: there few
-// tokens make up o, and their rounding would show as much as o's own.
+// ever rescaled and a job needs no maximum before its exponentials.  P is the sum of two bf16
+// parts (16 bits, as arkv_decode_attn holds it), which take all of S's place; each is multiplied
+// with V.  One part alone would be as coarse as o's own rounding, and show beside it whatever the
+// number of tokens.  The sum is of the unrounded values.
 //
 // Bound.  HBM for one tile of rows, the tensor cores for two (floors of a prefix of
 // 23701 bf16 and 18900 FP8 tokens, 8 key heads of 128: 21.2 us for 128 rows, 26.8 us for 256).
@@ -329,7 +328,7 @@ __device__ void multiply_qk(const Ctx& cx, const char* gsmem, uint32_t smem, uin
     }
 }
 
-template <int D, bool TWO, bool FINE>
+template <int D, bool TWO>
 __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uint32_t tmem) {
     using L = Smem<D, TWO>;
     constexpr uint32_t kIdPV = idesc_bf16(kRows, D, true);
@@ -364,7 +363,7 @@ __device__ void multiply_pv(const Ctx& cx, const char* gsmem, uint32_t smem, uin
             const bool add = x >= 2;   // each warpgroup's first product of the segment starts its O
             if (leader) {
 #pragma unroll
-                for (int k = 0; k < (FINE ? 2 : 1) * kTok / 16; ++k)
+                for (int k = 0; k < 2 * kTok / 16; ++k)   // the upper parts, then the lower ones
                     mma_ts(to, from + 8 * k, v_desc + (uint64_t)(k % (kTok / 16) * 128), kIdPV, add || k > 0);
                 if (!two || b == 1) commit(cx.bar(L::kEmptyB + s));
                 if (fp8 && (!two || b == 1)) commit(cx.bar(L::kScFree + (f - 1) % L::kScales));
@@ -556,7 +555,7 @@ __device__ __noinline__ void rescale(uint32_t o, float ff) {
 // A half is run again when its reference turns out wrong: too low, or, in a segment's first
 // job, which starts from zero, too high.  O (column o) then has to be idle: the product of the
 // job before has completed when it frees its V, entry pv.  False if that took too long.
-template <int D, bool FP8, bool TWO, bool FINE>
+template <int D, bool FP8, bool TWO>
 __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, uint32_t o, bool first, int valid,
                                             const float* sk, const float* sv, float c2, Rows& r) {
     const float2 cc = make_float2(c2, c2);
@@ -589,7 +588,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
             }
             float mx[2];
             float2 l[2];
-            uint32_t pa[16], pl[FINE ? 16 : 1];   // P of the two rows: [2 g + k]; what it lacks
+            uint32_t pa[16], pl[16];   // P of the two rows: [2 g + k], its upper and lower parts
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 mx[k] = kNegInf;
@@ -611,7 +610,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
                     if (FP8) p = mul2(p, vs);
                     const uint32_t hi = pack_bf16(p.x, p.y);
                     pa[2 * g + k] = hi;
-                    if constexpr (FINE) pl[2 * g + k] = pack_bf16(p.x - bf16_lo(hi), p.y - bf16_hi(hi));
+                    pl[2 * g + k] = pack_bf16(p.x - bf16_lo(hi), p.y - bf16_hi(hi));
                 }
             }
             bool move = false, low = false;
@@ -626,7 +625,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
 #pragma unroll
                 for (int k = 0; k < 2; ++k) r.l[k] += l[k].x + l[k].y;
                 tmem_st_16x128b_x8(s + half * (16u << 16), pa);   // over S, which has been read
-                if constexpr (FINE) tmem_st_16x128b_x8(s + kTok / 2 + half * (16u << 16), pl);
+                tmem_st_16x128b_x8(s + kTok / 2 + half * (16u << 16), pl);
                 break;
             }
             float f[2];
@@ -663,7 +662,7 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
     return true;
 }
 
-template <int D, bool TWO, bool FINE>
+template <int D, bool TWO>
 __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t tmem, int b) {
     using L = Smem<D, TWO>;
     const LayerDims& d = a.p.d;
@@ -700,9 +699,9 @@ __device__ void softmax(const AttnArgs& a, const Ctx& cx, char* smem, uint32_t t
             const int pv = 2 * (j + x - (two ? 1 : 2)) + 1;   // the V of this warpgroup's job before
             if (t.fp8) {
                 const float* sk = reinterpret_cast<const float*>(smem + L::kScale) + 2 * z * kTok;
-                if (!softmax_job<D, true, TWO, FINE>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
+                if (!softmax_job<D, true, TWO>(cx, pv, s + buf * kTok, o, first, t.valid, sk, sk + kTok, c2, r)) return;
             } else {
-                if (!softmax_job<D, false, TWO, FINE>(cx, pv, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r)) return;
+                if (!softmax_job<D, false, TWO>(cx, pv, s + buf * kTok, o, first, t.valid, nullptr, nullptr, c2, r)) return;
             }
             first = false;
             fence_before();
@@ -1016,7 +1015,7 @@ __device__ __noinline__ void no_prefix(const AttnArgs& a) {
     }
 }
 
-template <int D, int FMT, bool TWO, bool FINE>
+template <int D, int FMT, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ AttnArgs a) {
     using L = Smem<D, TWO>;
     extern __shared__ __align__(1024) char smem[];
@@ -1085,13 +1084,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             drain<D, TWO>(cx, 0);
         } else if (warp == 2) {
             pdl_wait();
-            multiply_pv<D, TWO, FINE>(cx, smem, base, uniform(tmem));
+            multiply_pv<D, TWO>(cx, smem, base, uniform(tmem));
             drain<D, TWO>(cx, 1);
         }
     } else if (warp < 12) {
         set_regs<144, true>();
         pdl_wait();
-        softmax<D, TWO, FINE>(a, cx, smem, tmem, (warp - 4) >> 2);
+        softmax<D, TWO>(a, cx, smem, tmem, (warp - 4) >> 2);
     } else {
         set_regs<56, false>();
         pdl_wait();
@@ -1286,13 +1285,12 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     if (e != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     long long ctas = sms < kMaxCtas ? sms : kMaxCtas;   // one an SM
-    const long long all = ctas;
     if (ctas > w.places) ctas = w.places;
     auto divisor = [](long long x) { return x == 1 ? 0u : (unsigned)(0x100000000ll / x + 1); };
     a.div_hkv = divisor(d.hkv);
     a.div_unit = divisor(per_unit);
     a.div_ctas = divisor(ctas);
-    static unsigned char done[16][64], done_join[16][64];
+    static unsigned char done[8][64], done_join[8][64];
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1315,22 +1313,15 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
         lc.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&lc, join, a);
     };
-    // P in two parts while the list, by the capacities, leaves an SM four places or fewer: such
-    // calls are latency (648 tokens, 2 key heads of 64: 9.3 us, 9.0 with one part; 2700 tokens, 8
-    // key heads of 128, 32 branches: 14.2 and 14.1), and few tokens make up o (error of o for the
-    // first of them 0.0016, 0.0023 with one part).
-    const bool fine = w.places <= 4 * all;
-    auto pick = [&](auto dim, auto fmt, auto two, auto parts, int which) {
+    auto pick = [&](auto dim, auto fmt, auto two, int which) {
         constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
-        constexpr bool T = decltype(two)::value, P2 = decltype(parts)::value;
-        return go(prefix_attn_kernel<D, F, T, P2>, prefix_join_kernel<D>, which, Smem<D, T>::kBytes);
+        constexpr bool T = decltype(two)::value;
+        return go(prefix_attn_kernel<D, F, T>, prefix_join_kernel<D>, which, Smem<D, T>::kBytes);
     };
     using std::integral_constant;
     auto with = [&](auto dim, auto fmt, int which) {
-        const std::true_type yes{};
-        const std::false_type no{};
-        if (fine) return w.row_tiles == 2 ? pick(dim, fmt, yes, yes, which + 12) : pick(dim, fmt, no, yes, which + 8);
-        return w.row_tiles == 2 ? pick(dim, fmt, yes, no, which + 4) : pick(dim, fmt, no, no, which);
+        if (w.row_tiles == 2) return pick(dim, fmt, std::true_type{}, which + 4);
+        return pick(dim, fmt, std::false_type{}, which);
     };
     const integral_constant<int, 128> d128{};
     const integral_constant<int, 64> d64{};
