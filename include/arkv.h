@@ -337,6 +337,7 @@ int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_c
  * float32.
  * The prefix is only read: its tokens are neither scored nor reassigned while it is
  * shared.  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
+ * Where a call sets ARKV_STATUS_TIMEOUT (in *prefix->status), its o and ml are unspecified.
  * The workspace holds at least arkv_prefix_workspace_bytes() bytes and needs no
  * preparation.  Launched as a programmatic dependent like arkv_decode_attn: with
  * cfg->early_start = 1 it reads the prefix cache and branch_start before the previous

@@ -51,6 +51,7 @@
 #include <cudaTypedefs.h>
 
 #include "arkv_internal.cuh"
+#include "prefix_join.h"
 #include "tc.cuh"
 
 namespace arkv {
@@ -1125,6 +1126,7 @@ __global__ void __launch_bounds__(4 * D) prefix_join_kernel(const __grid_constan
     // and visible to whatever that kernel reads ahead of its own wait.
     pdl_launch_dependents();
     const int4 info = __ldcg(a.join + blockIdx.x);
+    const JoinSpan span = join_span(info.x, info.y, info.z, a.slots, a.row_tiles, kRows, d.G);
     float M = kNegInf, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (part == 0 && a.p.ml_own && jq < d.G) {
@@ -1136,17 +1138,17 @@ __global__ void __launch_bounds__(4 * D) prefix_join_kernel(const __grid_constan
             acc = make_float4(L * o.x, L * o.y, L * o.z, L * o.w);
         }
     }
-    const int last = jq < d.G ? min(info.y, a.slots - 1) : -1;
-    for (int c = max(info.x, 0) + part; c <= last; c += 4 * kBatch) {
+    const int last = jq < d.G ? span.last : -1;
+    for (int c = span.first + part; c <= last; c += 4 * kBatch) {
         float2 ml[kBatch];
         float4 x[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             ml[q] = make_float2(kNegInf, 0.f);
             if (c + 4 * q <= last) {
-                const size_t s = (size_t)(c + 4 * q) * a.row_tiles + info.z / kRows;
-                ml[q] = __ldcg(a.part_ml + s * kRows + info.z % kRows + jq);
-                x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + info.z % kRows + jq);
+                const size_t s = (size_t)(c + 4 * q) * a.row_tiles + span.row / kRows;
+                ml[q] = __ldcg(a.part_ml + s * kRows + span.row % kRows + jq);
+                x[q] = __ldcg(a.part_o + (s * (D / 4) + c4) * kRows + span.row % kRows + jq);
             }
         }
         float mb = M;
