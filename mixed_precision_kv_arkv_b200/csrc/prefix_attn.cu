@@ -398,8 +398,9 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
     const int lane = threadIdx.x & 31;
     const uint32_t to = smem_u32(smem + L::kScale) + 4 * lane;
     int f = 0, j = 0, last = 0;   // FP8 tiles, tiles so far; the last FP8 tile
+    bool ok = true;
     Seg w{};
-    for (int seg = 0; warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
+    for (int seg = 0; ok && warp_segment<D, TWO>(cx, smem, seg, w); ++seg) {
         const float* sk = a.p.c.sk + (size_t)w.row * a.p.d.cap_q;
         const float* sv = a.p.c.sv + (size_t)w.row * a.p.d.cap_q;
         Tiles tiles(w);
@@ -408,13 +409,14 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
             const Tile t = tiles.next();
             if (!t.fp8) continue;
             const int z = f % L::kScales, use = f / L::kScales;
-            if (use > 0 && !cx.warp_wait(L::kScFree + z, (use - 1) & 1)) return;   // its last readers
+            ok = use == 0 || cx.warp_wait(L::kScFree + z, (use - 1) & 1);   // its last readers
+            if (!ok) break;
             // The slot's barrier has to be done with the FP8 tile that had the slot before.  In a run
             // of FP8 tiles that one is more than kScales back, so the wait above shows it; after bf16
             // tiles (of a new segment) every FP8 tile so far has to be done.
-            if (f > 0 && j + i > last + 1 &&
-                !cx.warp_wait(L::kScFree + (f - 1) % L::kScales, ((f - 1) / L::kScales) & 1))
-                return;
+            if (f > 0 && j + i > last + 1)
+                ok = cx.warp_wait(L::kScFree + (f - 1) % L::kScales, ((f - 1) / L::kScales) & 1);
+            if (!ok) break;
 #pragma unroll
             for (int c = 0; c < 2 * kTok; c += 32) {
                 const int tok = min(t.idx * kTok + (c & (kTok - 1)) + lane, w.n8 - 1);
@@ -426,7 +428,7 @@ __device__ void load_scales(const AttnArgs& a, const Ctx& cx, char* smem) {
         }
         j += tiles.n;
     }
-    cp_async_wait_all();
+    cp_async_wait_all();   // (also when it gives up)
 }
 
 // ------------------------------------------------------------------ FP8 -> bf16 (128 threads, two a token)
@@ -643,7 +645,10 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
                 }
             }
             if (!begin) {
-                if (!cx.warp_wait(Smem<D, TWO>::kEmptyB + pv % Smem<D, TWO>::kSlots, (pv / Smem<D, TWO>::kSlots) & 1)) return false;
+                if (!cx.warp_wait(Smem<D, TWO>::kEmptyB + pv % Smem<D, TWO>::kSlots, (pv / Smem<D, TWO>::kSlots) & 1)) {
+                    wait_st();
+                    return false;
+                }
                 fence_after();
                 const int lane = threadIdx.x & 31, src = 4 * (lane & 7);
                 const float f0 = __shfl_sync(kFull, f[0], src), f1 = __shfl_sync(kFull, f[1], src);
@@ -849,6 +854,7 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
     const LayerDims& d = a.p.d;
     const int per_unit = a.row_tiles * a.per_tile;
     int seg = 0, e = 0, m = 0;              // segments and entries so far; place of the unit in its row
+    int queries = 0;                        // loads of a segment's queries so far
     uint32_t ph[3] = {0, 0, 0}, last[3] = {0, 0, 0};   // by barrier (full, raw K, raw V): parity of each slot's next
                                                        // phase, the slots whose last load it has
     RowInfo r = s.r;
@@ -964,6 +970,7 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
                                     x.branch + q * a.per_tile, cx.bar(L::kQFull));
             }
             __syncwarp();
+            ++queries;
             if (seg >= L::kSegs && !(ok = cx.warp_wait(L::kSegEmpty + z, ((seg / L::kSegs) & 1) ^ 1))) continue;
             x.rows0 = min(left, a.per_tile) * d.G;
             x.rows1 = max(min(left - a.per_tile, a.per_tile), 0) * d.G;
@@ -986,8 +993,8 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
                 for (int k = 0; k < kSpinLimit && !mbar_try_wait(cx.bar((i == 0 ? L::kFullB : i == 1 ? L::kRawB : L::kRawB + L::kSlots) + z),
                                                                  ((ph[i] >> z) & 1u) ^ 1u); ++k) {
                 }
-    if (seg > 0)
-        for (int k = 0; k < kSpinLimit && !mbar_try_wait(cx.bar(L::kQFull), (seg - 1) & 1); ++k) {
+    if (queries > 0)
+        for (int k = 0; k < kSpinLimit && !mbar_try_wait(cx.bar(L::kQFull), (queries - 1) & 1); ++k) {
         }
 }
 
