@@ -61,6 +61,7 @@ namespace {
 using namespace tc;
 
 constexpr float kNegInf = -INFINITY;
+constexpr float kNoLogit = -32768.f;   // the reference of a row whose logits so far are all -inf: any rise from it is exact enough
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 128;            // query rows of a tile
 constexpr int kTok = 64;              // tokens of a tile
@@ -636,7 +637,8 @@ __device__ __forceinline__ bool softmax_job(const Ctx& cx, int pv, uint32_t s, u
             for (int k = 0; k < 2; ++k) {
                 const float t = quad_max(mx[k]);
                 if (begin) {
-                    r.m[k] = t != kNegInf && fabsf(t) > 32.f ? t : 0.f;   // (each row for itself)
+                    // (each row for itself; without any weight so far, below what a later logit has)
+                    r.m[k] = t == kNegInf ? kNoLogit : fabsf(t) > 32.f ? t : 0.f;
                 } else {
                     const float up = fmaxf(ceilf(t - r.m[k]), 0.f);
                     f[k] = ex2(-up);

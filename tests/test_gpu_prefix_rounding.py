@@ -204,3 +204,34 @@ def test_long_runs_with_a_rising_reference(cuda, d, G, prefixes, branches, fmt):
     again = run(c, prefix, q, starts)
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     assert int(prefix.status) == 0
+
+
+@pytest.mark.parametrize("d,branches,prefixes", [(128, 4, 1), (64, 40, 1), (128, 1, 20), (64, 40, 20)])
+def test_tokens_without_weight_first(cuda, d, branches, prefixes):
+    """The first 130 tokens have logits of -inf, the others all of about -140 (e^-140 is past float32's
+    range): the others make up the softmax.  A prefix of -inf alone has no weight: o = 0, (-inf, 0)."""
+    hkv, G, n16, n8 = 8, 4, 400, 300
+    pc = R.cfg(prefixes + 1, hkv * G, hkv, d, n16, n8)
+    prefix, u = heavy_prefix(pc, [n16] * prefixes + [70], [n8] * prefixes + [0], cuda, 90, heavy=0)
+    prefix.k16[prefixes * hkv:, :70, 0] = float("-inf")
+    g = gen(cuda, 91)
+    for r in range(prefixes * hkv):
+        k = -140 / math.sqrt(d) * u[r % hkv] + 0.2 * torch.randn((n16 + n8, d), generator=g, device=cuda)
+        prefix.k16[r] = k[:n16].bfloat16()
+        prefix.k16[r, :130, 0] = float("-inf")
+        s = k[n16:].abs().amax(-1) / 448.0
+        prefix.k8[r], prefix.sk[r] = (k[n16:] / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8), s
+    c = R.cfg(prefixes * branches + 1, hkv * G, hkv, d)
+    starts = [branches * i for i in range(prefixes + 1)] + [prefixes * branches + 1]
+    q = queries(c, u, cuda, 92, noise=0.1)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    finite = C.LayerCache(pc, cuda)   # what has weight: the reference is taken over it
+    for f in R.FIELDS16 + R.FIELDS8 + ("n_bf16", "n_fp8"):
+        getattr(finite, f).copy_(getattr(prefix, f))
+    finite.k16[:, :n16 - 130], finite.v16[:, :n16 - 130] = prefix.k16[:, 130:], prefix.v16[:, 130:]
+    finite.n_bf16.fill_(n16 - 130)
+    few = R.cfg(prefixes * branches, hkv * G, hkv, d)
+    ref = exact(few, finite, q[:few.batch], starts[:-1])
+    o, ml = run(c, prefix, q, starts)
+    check(few, (o[:-1], ml[:few.batch * hkv]), ref, 11)
+    assert (o[-1] == 0).all() and (ml[few.batch * hkv:, :, 0] == float("-inf")).all() and (ml[few.batch * hkv:, :, 1] == 0).all()
