@@ -113,6 +113,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _expect(name, t, dtype, device, numel):
+    """A tensor that a call reads or writes by its address alone."""
+    if t.dtype != dtype or t.device != device or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} on {device} with {numel} elements, not {t.dtype} on "
+                         f"{t.device} of shape {tuple(t.shape)} and strides {t.stride()}")
+
+
 def rope_frequencies(rot: int, theta: float, device) -> torch.Tensor:
     """theta ** (-2 i / rot) for the rot / 2 rotated pairs, float64 radians per position."""
     i = torch.arange(rot // 2, dtype=torch.float64)
@@ -123,24 +130,32 @@ def qk_norm_rope(cfg: abi.arkv_cfg, qkv, n_tok: int, freq, k, v, q=None, q_obs=N
                  k_weight=None, eps: float = 1e-6, interleaved=False, pos0=None, step: int = 0, length=None,
                  stream=None):
     """arkv_qk_norm_rope on torch tensors: qkv [batch * n_tok, >= (hq + 2 hkv) D] bf16 (unit stride in
-    its last dimension), freq [rot / 2] float64 or None, k, v (and q) [batch, heads, n, D] bf16."""
-    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.shape[0] != cfg.batch * n_tok:
-        raise ValueError("qkv must be [batch * n_tok, width] with unit stride in its last dimension")
+    its last dimension), freq [rot / 2] float64 or None, k, v (and q) [batch, heads, n, D] bf16, q_obs [batch, hq,
+    n_obs, D]; q_weight, k_weight [D] bf16, pos0, length [batch] int32.  All but qkv are contiguous."""
+    width = (cfg.hq + 2 * cfg.hkv) * cfg.head_dim
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.shape[0] != cfg.batch * n_tok or qkv.shape[1] < width:
+        raise ValueError(f"qkv must be [batch * n_tok, {width} or more] with unit stride in its last dimension")
+    if k.dim() != 4:
+        raise ValueError("k must be a contiguous [batch, heads, n, head_dim] tensor")
     for name, t, heads in (("q", q, cfg.hq), ("k", k, cfg.hkv), ("v", v, cfg.hkv), ("q_obs", q_obs, cfg.hq)):
         if t is None and name in ("q", "q_obs"):
             continue
         n = cfg.n_obs if name == "q_obs" else k.shape[2]
         if not t.is_contiguous() or tuple(t.shape) != (cfg.batch, heads, n, cfg.head_dim):
             raise ValueError(f"{name} must be a contiguous [batch, heads, n, head_dim] tensor")
-    for name, t, dt in (("qkv", qkv, torch.bfloat16), ("q", q, torch.bfloat16), ("k", k, torch.bfloat16),
-                        ("v", v, torch.bfloat16), ("q_obs", q_obs, torch.bfloat16),
-                        ("q_weight", q_weight, torch.bfloat16), ("k_weight", k_weight, torch.bfloat16),
-                        ("freq", freq, torch.float64), ("pos0", pos0, torch.int32), ("length", length, torch.int32)):
-        if t is not None and (t.dtype != dt or t.device != qkv.device):
-            raise ValueError(f"{name} must be {dt} on {qkv.device}")
+    for name, t in (("qkv", qkv), ("q", q), ("k", k), ("v", v), ("q_obs", q_obs)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.device != qkv.device):
+            raise ValueError(f"{name} must be {torch.bfloat16} on {qkv.device}")
+    for name, t, dt, n in (("q_weight", q_weight, torch.bfloat16, cfg.head_dim),
+                           ("k_weight", k_weight, torch.bfloat16, cfg.head_dim),
+                           ("pos0", pos0, torch.int32, cfg.batch), ("length", length, torch.int32, cfg.batch)):
+        if t is not None:
+            _expect(name, t, dt, qkv.device, n)
+    if freq is not None:   # (rot <= head_dim is the library's check)
+        _expect("freq", freq, torch.float64, qkv.device, freq.numel())
     guard, s = _on_device(qkv, stream)
     with guard:
-        abi.arkv_qk_norm_rope(cfg, n_tok, qkv.data_ptr(), qkv.stride(0), _ptr(pos0), step, _ptr(length),
+        abi.arkv_qk_norm_rope(cfg, n_tok, qkv.data_ptr(), qkv.stride(0) if qkv.shape[0] > 1 else width, _ptr(pos0), step, _ptr(length),
                               _ptr(q_weight), _ptr(k_weight), eps, _ptr(freq), 0 if freq is None else 2 * freq.numel(),
                               int(bool(interleaved)), k.shape[2], _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_obs), s)
 

@@ -1,0 +1,60 @@
+"""The torch helpers refuse tensors whose addresses alone would not say what the caller means --
+strided, too short, of another type -- before anything is launched.  No CUDA device is touched: the
+tensors are on the host, and each refusal names the tensor (a call whose tensors are all in order
+is refused for the device)."""
+import pytest
+import torch
+
+from mixed_precision_kv_arkv_b200 import abi, build
+from mixed_precision_kv_arkv_b200 import cache as C
+
+BF, I32, F32, F64 = torch.bfloat16, torch.int32, torch.float32, torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    abi.lib()
+
+
+def z(*s, dt=BF):
+    return torch.zeros(s, dtype=dt)
+
+
+B, HQ, HKV, D, N, OBS = 3, 4, 2, 64, 5, 7
+W = (HQ + 2 * HKV) * D
+
+
+def rope_args():
+    return dict(qkv=z(B * N, W + 8), n_tok=N, freq=z(32, dt=F64), k=z(B, HKV, N, D), v=z(B, HKV, N, D), q=z(B, HQ, N, D),
+                q_obs=z(B, HQ, OBS, D), q_weight=z(D), k_weight=z(D), pos0=z(B, dt=I32), length=z(B, dt=I32))
+
+
+def rope(**bad):
+    a = {**rope_args(), **bad}
+    c = C.make_cfg(B, HQ, HKV, D, 16, OBS, 1.0, 0.5, 1, 1)
+    C.qk_norm_rope(c, a.pop("qkv"), a.pop("n_tok"), a.pop("freq"), a.pop("k"), a.pop("v"), **a)
+
+
+def test_rope_takes_tensors_in_order():
+    for ok in (dict(), dict(qkv=z(B * N, W)), dict(qkv=z(B * N, W + 64)[:, 8:8 + W]), dict(freq=None), dict(q=None, q_obs=None),
+               dict(q_weight=None, k_weight=None, pos0=None, length=None), dict(q_weight=z(2 * D)[D:], pos0=z(9, dt=I32)[2:5])):
+        with pytest.raises(ValueError, match="CUDA device"):
+            rope(**ok)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("pos0", z(B, 2, dt=I32)[:, 0]), ("pos0", z(B - 1, dt=I32)), ("pos0", z(B + 1, dt=I32)), ("pos0", z(B, dt=torch.int64)),
+    ("pos0", z(1, dt=I32).expand(B)),
+    ("length", z(B, 2, dt=I32)[:, 1]), ("length", z(1, dt=I32)), ("length", z(B, dt=F32)),
+    ("freq", z(64, dt=F64)[::2]), ("freq", z(32, 2, dt=F64)[:, 0]), ("freq", z(32, dt=F32)),
+    ("q_weight", z(D // 2)), ("q_weight", z(2 * D)[::2]), ("q_weight", z(D, dt=F32)),
+    ("k_weight", z(D - 1)), ("k_weight", z(1).expand(D)),
+    ("qkv", z(B * N, W - 8)), ("qkv", z(B * N, W + 64)[:, :W - 64]), ("qkv", z(B * N - 1, W)), ("qkv", z(B * N, 2 * W)[:, ::2]),
+    ("qkv", z(B * N * W)),
+    ("k", z(B, HKV, N * D)), ("k", z(B, N, HKV, D).transpose(1, 2)), ("v", z(B, HKV, N, D + 64)[..., :D]),
+    ("q", z(B, HQ, N + 1, D)), ("q_obs", z(B, HQ, N, D)),
+])
+def test_rope_refuses(name, bad):
+    with pytest.raises(ValueError, match=rf"^{name} must be"):
+        rope(**{name: bad})
