@@ -199,11 +199,22 @@ def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new
     """One decode step of one layer whose sequences share prefixes: append + attend to the own
     tokens (o_own, float32), attend to the prefix and join (o, bf16, and the heads' (max, sum) in
     the decode workspace), score update of the own tokens, and their reassignment when
-    (step + 1) % reassign_interval == 0.  ctx_len counts the prefix's tokens."""
-    for name, t, dt in (("q", q, torch.bfloat16), ("k_new", k_new, torch.bfloat16), ("v_new", v_new, torch.bfloat16),
-                        ("ctx_len", ctx_len, torch.int32), ("o_own", o_own, torch.float32), ("o", o, torch.bfloat16)):
-        if t.dtype != dt or t.device != q.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dt} on {q.device}")
+    (step + 1) % reassign_interval == 0.  ctx_len counts the prefix's tokens.  All tensors are contiguous:
+    q, o_own, o [batch, hq, D], k_new, v_new [batch, hkv, D] (or any shape of as many elements)."""
+    c, dev = st.cfg, st.cache.k16.device
+    nq, nkv = c.batch * c.hq * c.head_dim, c.batch * c.hkv * c.head_dim
+    for name, t, dt, n in (("q", q, torch.bfloat16, nq), ("k_new", k_new, torch.bfloat16, nkv),
+                           ("v_new", v_new, torch.bfloat16, nkv), ("ctx_len", ctx_len, torch.int32, c.batch),
+                           ("o_own", o_own, torch.float32, nq), ("o", o, torch.bfloat16, nq)):
+        _expect(name, t, dt, dev, n)
+    if tier_dbg is not None:
+        _expect("tier_dbg", tier_dbg, torch.uint8, dev, c.batch * c.hkv * (c.cap_bf16 + c.cap_fp8))
+    # what the later calls would refuse is refused before the first one appends
+    need = abi.arkv_prefix_workspace_bytes(c, prefix.cache.cfg)
+    if prefix.cache.k16.device != dev or need == 0 or prefix.ws.nbytes < need:
+        raise ValueError("prefix must be on the device of the branches' cache and made for their configuration")
+    if o.data_ptr() % 16:
+        raise ValueError("o must be 16-byte aligned")
     guard, s = _on_device(q, stream)
     with guard:
         abi.arkv_decode_attn(st.cfg, step, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), ctx_len.data_ptr(),

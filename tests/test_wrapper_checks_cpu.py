@@ -58,3 +58,46 @@ def test_rope_takes_tensors_in_order():
 def test_rope_refuses(name, bad):
     with pytest.raises(ValueError, match=rf"^{name} must be"):
         rope(**{name: bad})
+
+
+def branch_args():
+    return dict(q=z(B, HQ, D), k_new=z(B, HKV, 1, D), v_new=z(B, HKV, D), ctx_len=z(B, dt=I32), o_own=z(B, HQ, D, dt=F32),
+                o=z(B, HQ, D))
+
+
+def branch(prefix=None, **bad):
+    c = C.make_cfg(B, HQ, HKV, D, 4, 4, 1.0, 0.5, 20, 30)
+    st = C.new_layer_state(c, 0.5, "cpu")
+    if prefix is None:
+        prefix = C.new_shared_prefix(c, C.LayerCache(C.make_cfg(1, HQ, HKV, D, 4, 4, 1.0, 0.5, 9, 9), "cpu"))
+    C.branch_step(st, prefix, 0, **{**branch_args(), **bad}, reassign_interval=4)
+
+
+def test_branch_step_takes_tensors_in_order():
+    for ok in (dict(), dict(tier_dbg=z(B * HKV, 50, dt=torch.uint8)), dict(q=z(B, HQ, 1, D), o=z(B, HQ * D))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            branch(**ok)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", z(B, HQ, D // 2)), ("q", z(B - 1, HQ, D)), ("q", z(B, HQ, D, dt=F32)), ("q", z(B, D, HQ).transpose(1, 2)),
+    ("k_new", z(B, HQ, D)), ("k_new", z(B, HKV, 2 * D)[..., :D]), ("v_new", z(B, 1, D)), ("v_new", z(B, HKV, 1)),
+    ("ctx_len", z(B, 2, dt=I32)[:, 0]), ("ctx_len", z(B - 1, dt=I32)), ("ctx_len", z(B, dt=torch.int64)),
+    ("o_own", z(B, HQ, D)), ("o_own", z(B, HKV, D, dt=F32)), ("o", z(B, HKV, D)), ("o", z(1, 1, D).expand(B, HQ, D)),
+    ("o", z(B, HQ, D, dt=F32)), ("o", z(B * HQ * D + 4)[4:]), ("tier_dbg", z(B * HKV, 20, dt=torch.uint8)),
+    ("tier_dbg", z(B * HKV, 50)), ("o", torch.zeros((B, HQ, D), dtype=BF, device="meta")),
+])
+def test_branch_step_refuses(name, bad):
+    with pytest.raises(ValueError, match=rf"^{name} must be"):
+        branch(**{name: bad})
+
+
+def test_branch_step_refuses_prefixes_of_others():
+    mk = lambda batch, hq, dev: C.LayerCache(C.make_cfg(batch, hq, HKV, D, 4, 4, 1.0, 0.5, 9, 9), dev)   # noqa: E731
+    need = abi.arkv_prefix_workspace_bytes(C.make_cfg(B, HQ, HKV, D, 4, 4, 1.0, 0.5, 20, 30), mk(1, HQ, "cpu").cfg)
+    short = C.SharedPrefix(mk(1, HQ, "cpu"), None, C.Workspace(need - 1, "cpu"))
+    other = C.make_cfg(B, 2 * HQ, HKV, D, 4, 4, 1.0, 0.5, 20, 30)
+    elsewhere = C.SharedPrefix(mk(1, HQ, "meta"), None, C.Workspace(1 << 24, "cpu"))
+    for prefix in (short, C.new_shared_prefix(other, mk(1, 2 * HQ, "cpu")), elsewhere):
+        with pytest.raises(ValueError, match="^prefix must be"):
+            branch(prefix=prefix)
