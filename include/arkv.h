@@ -336,7 +336,7 @@ int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_c
  * product with V as the sum of two bf16 parts (16 bits, as in arkv_decode_attn); sums are
  * float32.
  * The prefix is only read: its tokens are neither scored nor reassigned while it is
- * shared.  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
+ * shared (the branches' own tokens: arkv_branch_reassign).  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
  * Where a call sets ARKV_STATUS_TIMEOUT (in *prefix->status), its o and ml are unspecified.
  * The workspace holds at least arkv_prefix_workspace_bytes() bytes and needs no
  * preparation.  Launched as a programmatic dependent like arkv_decode_attn: with
@@ -354,6 +354,22 @@ int arkv_prefix_attn(const arkv_cfg *cfg, const arkv_cfg *prefix_cfg, const uint
  * arkv_score_update: *ml = [batch * hkv][4][2] float within ws (p = exp((raw - M) /
  * sqrt(D)) / L).  Host only. */
 int arkv_decode_ml(const arkv_cfg *cfg, void *ws, size_t ws_bytes, float **ml);
+
+/* arkv_reassign for branches that share prefixes: the bytes of its prefix's live tokens are part
+ * of a branch's budget, as a copy's would be.  ctx_len counts the prefix's tokens; in the
+ * counts of arkv_quantize_pack
+ *   Rb = beta*N*4D - W*4D - (n_bf16*4D + n_fp8*(2D+8) of the prefix's row)
+ * and everything else is as in arkv_reassign.  A branch without a prefix: arkv_reassign.
+ * prefix_cfg, prefix and branch_start as in arkv_prefix_attn; of the prefix only the counts
+ * are read.
+ * Capacities of the branches: arkv_row_capacity for the whole context always suffices.
+ * Where every prefix was packed with this cfg's budget_frac and window and the same r, and its
+ * budget (not its length) set its counts, arkv_row_capacity for the own tokens and
+ * 2 / budget_frac more does. */
+int arkv_branch_reassign(const arkv_cfg *cfg, int32_t step, float r, const int32_t *ctx_len,
+                         arkv_layer_cache *cache, const arkv_cfg *prefix_cfg,
+                         const arkv_layer_cache *prefix, const int32_t *branch_start,
+                         uint8_t *tier_dbg, void *ws, size_t ws_bytes, arkv_stream_t stream);
 
 /* Message of the calling thread's last failure ("" if none). */
 const char *arkv_last_error_string(void);

@@ -67,6 +67,8 @@ _SIG = {
     "arkv_cache_fork": (ctypes.c_int, [_P, _P, _P, _P, _P, _P]),
     "arkv_prefix_workspace_bytes": (ctypes.c_size_t, [_P, _P]),
     "arkv_prefix_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "arkv_branch_reassign": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P,
+                                            ctypes.c_size_t, _P]),
     "arkv_decode_ml": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "arkv_last_error_string": (ctypes.c_char_p, []),
 }
@@ -187,6 +189,13 @@ def arkv_prefix_attn(cfg, prefix_cfg, q, prefix, branch_start, o_own, ml_own, o,
     rc = lib().arkv_prefix_attn(_ref(cfg), _ref(prefix_cfg), q, _ref(prefix), branch_start, o_own, ml_own, o,
                                 ml, ws, ws_bytes, stream)
     return _check("arkv_prefix_attn", rc) if check else rc
+
+
+def arkv_branch_reassign(cfg, step, r, ctx_len, cache, prefix_cfg, prefix, branch_start, tier_dbg, ws, ws_bytes,
+                         stream, check=True) -> int:
+    rc = lib().arkv_branch_reassign(_ref(cfg), step, r, ctx_len, _ref(cache), _ref(prefix_cfg), _ref(prefix),
+                                    branch_start, tier_dbg, ws, ws_bytes, stream)
+    return _check("arkv_branch_reassign", rc) if check else rc
 
 
 def arkv_decode_ml(cfg, ws, ws_bytes) -> int:

@@ -199,7 +199,8 @@ def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new
     """One decode step of one layer whose sequences share prefixes: append + attend to the own
     tokens (o_own, float32), attend to the prefix and join (o, bf16, and the heads' (max, sum) in
     the decode workspace), score update of the own tokens, and their reassignment when
-    (step + 1) % reassign_interval == 0.  ctx_len counts the prefix's tokens.  All tensors are contiguous:
+    (step + 1) % reassign_interval == 0 (the prefix's bytes are part of the budget, see arkv_branch_reassign, which
+    also says how to size the own cache).  ctx_len counts the prefix's tokens.  All tensors are contiguous:
     q, o_own, o [batch, hq, D], k_new, v_new [batch, hkv, D] (or any shape of as many elements)."""
     c, dev = st.cfg, st.cache.k16.device
     nq, nkv = c.batch * c.hq * c.head_dim, c.batch * c.hkv * c.head_dim
@@ -225,5 +226,6 @@ def branch_step(st: LayerState, prefix: SharedPrefix, step: int, q, k_new, v_new
         abi.arkv_score_update(st.cfg, step, ctx_len.data_ptr(), st.cache.c, st.ws_decode.ptr,
                               st.ws_decode.nbytes, s)
         if (step + 1) % reassign_interval == 0:
-            abi.arkv_reassign(st.cfg, step, st.r, ctx_len.data_ptr(), st.cache.c, _ptr(tier_dbg),
-                              st.ws_reassign.ptr, st.ws_reassign.nbytes, s)
+            abi.arkv_branch_reassign(st.cfg, step, st.r, ctx_len.data_ptr(), st.cache.c, prefix.cache.cfg, prefix.cache.c,
+                                     _ptr(prefix.branch_start), _ptr(tier_dbg), st.ws_reassign.ptr,
+                                     st.ws_reassign.nbytes, s)

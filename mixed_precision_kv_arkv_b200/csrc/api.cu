@@ -231,24 +231,30 @@ int arkv_score_update(const arkv_cfg* cfg, int32_t step, const int32_t* ctx_len,
     return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_score_update");
 }
 
-int arkv_reassign(const arkv_cfg* cfg, int32_t step, float r, const int32_t* ctx_len, arkv_layer_cache* cache,
-                  uint8_t* tier_dbg, void* ws, size_t ws_bytes, arkv_stream_t stream) {
-    ARKV_TRY(check_cfg(cfg));
-    ARKV_TRY(check_cache(cache));
-    if (!ctx_len) return fail(ARKV_EINVAL, "%s: null argument", "arkv_reassign");
-    if (!(r >= 0.f && r <= 1.f)) return fail(ARKV_EINVAL, "%s: r must be in [0, 1]", "arkv_reassign");
-    if (step < 0) return fail(ARKV_EINVAL, "%s: step < 0", "arkv_reassign");
+static int reassign(const char* name, const arkv_cfg* cfg, int32_t step, float r, const int32_t* ctx_len,
+                    arkv_layer_cache* cache, const arkv::SharedPrefixes& shared, uint8_t* tier_dbg, void* ws,
+                    size_t ws_bytes, arkv_stream_t stream) {
+    if (!ctx_len) return fail(ARKV_EINVAL, "%s: null argument", name);
+    if (!(r >= 0.f && r <= 1.f)) return fail(ARKV_EINVAL, "%s: r must be in [0, 1]", name);
+    if (step < 0) return fail(ARKV_EINVAL, "%s: step < 0", name);
     const arkv::LayerDims d = dims(cfg);
     const size_t need = arkv::reassign_ws_bytes(d);
     ARKV_TRY(check_ws(ws, ws_bytes, need));
     arkv::ReassignParams p{};
-    p.d = d; p.step = step; p.r = r; p.ctx_len = ctx_len; p.c = *cache; p.tier_dbg = tier_dbg;
+    p.d = d; p.step = step; p.r = r; p.ctx_len = ctx_len; p.c = *cache; p.shared = shared; p.tier_dbg = tier_dbg;
     const size_t slots = (size_t)(d.cap_o + d.cap_q);
     const size_t idx_bytes = (slots * 2 * 4 * d.R + 255) & ~(size_t)255;
     p.idx_ws = (int32_t*)ws;
     p.key_ws = (uint64_t*)((char*)ws + idx_bytes);
     const cudaError_t e = arkv::launch_reassign(p, (cudaStream_t)stream);
-    return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_reassign");
+    return e == cudaSuccess ? ARKV_OK : cuda_fail(e, name);
+}
+
+int arkv_reassign(const arkv_cfg* cfg, int32_t step, float r, const int32_t* ctx_len, arkv_layer_cache* cache,
+                  uint8_t* tier_dbg, void* ws, size_t ws_bytes, arkv_stream_t stream) {
+    ARKV_TRY(check_cfg(cfg));
+    ARKV_TRY(check_cache(cache));
+    return reassign("arkv_reassign", cfg, step, r, ctx_len, cache, arkv::SharedPrefixes{}, tier_dbg, ws, ws_bytes, stream);
 }
 
 // True if the device can address ptr: device memory, or page-locked host memory mapped
@@ -336,11 +342,11 @@ int arkv_cache_fork(const arkv_cfg* dst_cfg, arkv_layer_cache* dst, const arkv_c
     return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_cache_fork");
 }
 
-static int check_prefix_cfg(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg) {
+static int check_prefix_cfg(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, const char* name = "arkv_prefix_attn") {
     ARKV_TRY(check_cfg(cfg));
     ARKV_TRY(check_cfg(prefix_cfg));
     if (cfg->hq != prefix_cfg->hq || cfg->hkv != prefix_cfg->hkv || cfg->head_dim != prefix_cfg->head_dim)
-        return fail(ARKV_EINVAL, "%s: hq, hkv and head_dim of the branches and the prefixes differ", "arkv_prefix_attn");
+        return fail(ARKV_EINVAL, "%s: hq, hkv and head_dim of the branches and the prefixes differ", name);
     return ARKV_OK;
 }
 
@@ -372,6 +378,21 @@ int arkv_prefix_attn(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, const uint
     p.early_start = cfg->early_start;
     const cudaError_t e = arkv::launch_prefix_attn(p, ws, (cudaStream_t)stream);
     return e == cudaSuccess ? ARKV_OK : cuda_fail(e, "arkv_prefix_attn");
+}
+
+int arkv_branch_reassign(const arkv_cfg* cfg, int32_t step, float r, const int32_t* ctx_len, arkv_layer_cache* cache,
+                         const arkv_cfg* prefix_cfg, const arkv_layer_cache* prefix, const int32_t* branch_start,
+                         uint8_t* tier_dbg, void* ws, size_t ws_bytes, arkv_stream_t stream) {
+    ARKV_TRY(check_prefix_cfg(cfg, prefix_cfg, "arkv_branch_reassign"));
+    ARKV_TRY(check_cache(cache));
+    ARKV_TRY(check_cache(prefix));
+    if (!branch_start && prefix_cfg->batch != 1)
+        return fail(ARKV_EINVAL, "%s: several prefixes need branch_start", "arkv_branch_reassign");
+    if (!aligned(branch_start, 4)) return fail(ARKV_EINVAL, "%s: branch_start is misaligned", "arkv_branch_reassign");
+    arkv::SharedPrefixes s{};
+    s.n = prefix_cfg->batch; s.cap_o = prefix_cfg->cap_bf16; s.cap_q = prefix_cfg->cap_fp8;
+    s.n_bf16 = prefix->n_bf16; s.n_fp8 = prefix->n_fp8; s.branch_start = branch_start;
+    return reassign("arkv_branch_reassign", cfg, step, r, ctx_len, cache, s, tier_dbg, ws, ws_bytes, stream);
 }
 
 int arkv_decode_ml(const arkv_cfg* cfg, void* ws, size_t ws_bytes, float** ml) {

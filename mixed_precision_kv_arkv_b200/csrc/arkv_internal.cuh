@@ -54,13 +54,14 @@ __device__ __forceinline__ double score_f64(double mu, double m2, int n, float g
 }
 
 // Budget counts of one row, float64 with the operations in a fixed order so that
-// every implementation doing the same operations obtains the same integers.
+// every implementation doing the same operations obtains the same integers.  `held`:
+// bytes of the budget that a shared prefix keeps (a whole number; 0 changes nothing).
 __host__ __device__ inline void budget_counts(float beta, int n_t, float r, int D, int W,
-                                              int n_cand, int* n_sel, int* n_o) {
+                                              int n_cand, int* n_sel, int* n_o, double held = 0.0) {
     const double b_o = 4.0 * D, b_q = 2.0 * D + 8.0;
 #ifdef __CUDA_ARCH__
-    const double rb = __dsub_rn(__dmul_rn(__dmul_rn((double)beta, (double)n_t), b_o),
-                                __dmul_rn((double)W, b_o));
+    const double rb = __dsub_rn(__dsub_rn(__dmul_rn(__dmul_rn((double)beta, (double)n_t), b_o),
+                                          __dmul_rn((double)W, b_o)), held);
     const double denom = __dadd_rn(__dmul_rn((double)r, b_o),
                                    __dmul_rn(__dsub_rn(1.0, (double)r), b_q));
     long long ns = rb > 0 ? (long long)floor(__ddiv_rn(rb, denom)) : 0;
@@ -68,7 +69,8 @@ __host__ __device__ inline void budget_counts(float beta, int n_t, float r, int 
     volatile double t1 = (double)beta * (double)n_t;
     volatile double t2 = t1 * b_o;
     volatile double t3 = (double)W * b_o;
-    const double rb = t2 - t3;
+    volatile double t4 = t2 - t3;
+    const double rb = t4 - held;
     volatile double d1 = (double)r * b_o;
     volatile double d2 = (1.0 - (double)r) * b_q;
     const double denom = d1 + d2;
@@ -168,12 +170,20 @@ cudaError_t launch_decode_attn(AttnParams& p, cudaStream_t s);   // fills the te
 cudaError_t launch_score_update(const ScoreParams& p, cudaStream_t s);
 cudaError_t launch_copy16(void* dst, const void* src, size_t bytes, cudaStream_t s);   // bytes % 16 == 0
 
+// The prefixes that a call's sequences (branches) share; n = 0: none.
+struct SharedPrefixes {
+    int n, cap_o, cap_q;
+    const int32_t *n_bf16, *n_fp8;   // [n * hkv] live slots
+    const int32_t* branch_start;     // [n + 1], nullable with one prefix: every branch
+};
+
 struct ReassignParams {
     LayerDims d;
     int step;
     float r;
     const int32_t* ctx_len;
     arkv_layer_cache c;
+    SharedPrefixes shared;
     uint8_t* tier_dbg;
     uint64_t* key_ws;   // [R][cap_o + cap_q] keys (used when they do not fit in shared memory)
     int32_t* idx_ws;    // [R][2][cap_o + cap_q] scratch slot lists

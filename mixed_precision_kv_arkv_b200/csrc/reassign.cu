@@ -268,6 +268,24 @@ __device__ __forceinline__ float warp_quantize_row(const uint16_t* src, uint8_t*
 }
 
 // ------------------------------------------------------------------ reassignment
+// The bytes of row (b, g)'s budget that branch b's prefix keeps (whole numbers, exact in float64).
+__device__ __forceinline__ double prefix_bytes(const SharedPrefixes& s, int b, int g, int hkv, int D) {
+    if (s.n == 0) return 0.0;
+    int pre = 0;
+    if (s.branch_start) {   // the last prefix that starts at or before b, if b is one of its branches
+        int hi = s.n;
+        while (hi - pre > 1) {
+            const int mid = (pre + hi) / 2;
+            if (s.branch_start[mid] <= b) pre = mid;
+            else hi = mid;
+        }
+        if (b < s.branch_start[pre] || b >= s.branch_start[pre + 1]) return 0.0;
+    }
+    const size_t row = (size_t)pre * hkv + g;
+    const double n16 = min(max(s.n_bf16[row], 0), s.cap_o), n8 = min(max(s.n_fp8[row], 0), s.cap_q);
+    return n16 * (4.0 * D) + n8 * (2.0 * D + 8.0);
+}
+
 constexpr int kKeyBatch = 8;   // slots per thread whose loads are in flight together (key build)
 
 // Slot outcomes, frozen before any data moves.
@@ -327,7 +345,7 @@ __global__ void __launch_bounds__(kRowThreads) reassign_kernel(const ReassignPar
     ncand = block_sum(ncand, sh);
     if (tid == 0) {
         int n_sel, n_o;
-        budget_counts(d.beta, nt, p.r, d.D, d.W, ncand, &n_sel, &n_o);
+        budget_counts(d.beta, nt, p.r, d.D, d.W, ncand, &n_sel, &n_o, prefix_bytes(p.shared, b, row - b * d.hkv, d.hkv, d.D));
         sh.misc[0] = n_sel;
         sh.misc[1] = n_o;
     }
