@@ -323,6 +323,9 @@ int arkv_cache_fork(const arkv_cfg* dst_cfg, arkv_layer_cache* dst, const arkv_c
     if (dst_cfg->hkv != src_cfg->hkv || dst_cfg->head_dim != src_cfg->head_dim ||
         dst_cfg->quant_format != src_cfg->quant_format)
         return fail(ARKV_EINVAL, "%s: hkv, head_dim and quant_format of the two caches differ", "arkv_cache_fork");
+    // (rows, and blocks of a row at least one, in 31 bits)
+    if ((int64_t)dst_cfg->batch * dst_cfg->hkv > INT_MAX || (int64_t)src_cfg->batch * src_cfg->hkv > INT_MAX - (1 << 20))
+        return fail(ARKV_EINVAL, "%s: batch * hkv must fit in 31 bits", "arkv_cache_fork");
     // one cache or two: every buffer the same (and the shapes with it), or none
     const void* a[] = {dst->k16, dst->v16, dst->pos16, dst->mu16, dst->m2_16, dst->k8, dst->v8, dst->sk, dst->sv,
                        dst->pos8, dst->mu8, dst->m2_8, dst->n_bf16, dst->n_fp8};
@@ -350,8 +353,14 @@ static int check_prefix_cfg(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, con
     return ARKV_OK;
 }
 
+static int check_prefix_sizes(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg) {
+    if (!arkv::prefix_sizes_fit(dims(prefix_cfg), cfg->batch))
+        return fail(ARKV_EINVAL, "%s: prefix rows times capacity and the list of all tiles must fit in 31 bits", "arkv_prefix_attn");
+    return ARKV_OK;
+}
+
 size_t arkv_prefix_workspace_bytes(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg) {
-    if (check_prefix_cfg(cfg, prefix_cfg) != ARKV_OK) return 0;
+    if (check_prefix_cfg(cfg, prefix_cfg) != ARKV_OK || check_prefix_sizes(cfg, prefix_cfg) != ARKV_OK) return 0;
     return arkv::prefix_ws_bytes(dims(prefix_cfg), cfg->batch);
 }
 
@@ -367,9 +376,8 @@ int arkv_prefix_attn(const arkv_cfg* cfg, const arkv_cfg* prefix_cfg, const uint
     if (!aligned(q, 16) || !aligned(o_own, 16) || !aligned(o, 16) || !aligned(ml_own, 8) || !aligned(ml, 8) ||
         !aligned(branch_start, 4))
         return fail(ARKV_EINVAL, "%s: q, o_own and o must be 16-byte, ml 8-byte aligned", "arkv_prefix_attn");
+    ARKV_TRY(check_prefix_sizes(cfg, prefix_cfg));
     const arkv::LayerDims d = dims(prefix_cfg);
-    if ((int64_t)d.R * d.cap_o > INT_MAX - 256 || (int64_t)d.R * d.cap_q > INT_MAX - 256)
-        return fail(ARKV_EINVAL, "%s: prefix rows times capacity must fit in 31 bits", "arkv_prefix_attn");
     ARKV_TRY(check_ws(ws, ws_bytes, arkv::prefix_ws_bytes(d, cfg->batch)));
     arkv::PrefixParams p{};
     p.d = d; p.branches = cfg->batch; p.q = q; p.c = *prefix; p.branch_start = branch_start;

@@ -265,6 +265,7 @@ struct PrefixParams {
     double inv_sqrt_d;
     int early_start;
 };
+bool prefix_sizes_fit(const LayerDims& d, int branches);
 size_t prefix_ws_bytes(const LayerDims& d, int branches);
 cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s);
 

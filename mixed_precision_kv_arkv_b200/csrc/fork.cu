@@ -153,7 +153,6 @@ cudaError_t launch_cache_fork(const ForkParams& p, cudaStream_t s) {
     const long long rows = (long long)p.src_batch * p.hkv, most = (8ll * 4 * 148 + rows - 1) / rows;
     const int per_row = (int)(pc.total() < most ? pc.total() : most);
     const long long blocks = rows * per_row;
-    if (blocks > 0x7fffffff || (long long)p.dst_batch * p.hkv > 0x7fffffff) return cudaErrorInvalidValue;
     cache_fork_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(p, pc, per_row);
     return cudaGetLastError();
 }

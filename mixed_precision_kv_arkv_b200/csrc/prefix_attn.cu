@@ -1268,6 +1268,15 @@ PrefixWs ws_layout(const LayerDims& d, int branches) {
 
 }  // namespace
 
+// Whether the kernels' 32-bit places, rows and divisions hold for these sizes.
+bool prefix_sizes_fit(const LayerDims& d, int branches) {
+    const PrefixWs w = ws_layout(d, branches);
+    const long long blocks = (long long)branches * d.hkv, rows = (long long)d.batch * d.hkv;
+    const long long per_unit = (long long)w.row_tiles * w.per_tile;
+    return w.places <= 0x7fffffff && blocks <= 0x7fffffff && blocks * d.hkv <= 0xffffffffll && rows * d.hkv <= 0xffffffffll &&
+           (branches + per_unit) * per_unit <= 0xffffffffll && rows * d.cap_o <= 0x7fffffff - 256 &&
+           rows * d.cap_q <= 0x7fffffff - 256;
+}
 size_t prefix_ws_bytes(const LayerDims& d, int branches) { return ws_layout(d, branches).total; }
 
 cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) {
@@ -1275,9 +1284,6 @@ cudaError_t launch_prefix_attn(const PrefixParams& p, void* ws, cudaStream_t s) 
     const PrefixWs w = ws_layout(d, p.branches);
     const long long blocks = (long long)p.branches * d.hkv;
     const long long per_unit = (long long)w.row_tiles * w.per_tile;
-    if (w.places > 0x7fffffff || blocks * d.hkv > 0xffffffffll || (long long)d.R * d.hkv > 0xffffffffll ||
-        (p.branches + per_unit) * per_unit > 0xffffffffll)
-        return cudaErrorInvalidValue;
     AttnArgs a{};
     a.p = p;
     a.slots = (int)w.slots;
