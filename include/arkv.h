@@ -302,8 +302,9 @@ int arkv_qk_norm_rope(const arkv_cfg *cfg, int32_t n_tok, const uint16_t *qkv, i
  * configuration): then a sequence may only be copied if it keeps its own state in this call
  * (src_seq[s] = s or ARKV_SEQ_KEEP).  A sequence with another src_seq, or whose source does
  * not keep its state, stays as it was and ARKV_STATUS_BAD_FORK is set.
- * Slots past a count stay as they were.  The two configurations agree in hkv, head_dim and
- * quant_format; batch and capacities may differ: the slots past a smaller capacity are
+ * Slots past a count stay as they were.  The two configurations agree in hkv, head_dim,
+ * quant_format and n_obs (a token's count of observations is a function of it);
+ * batch and capacities may differ: the slots past a smaller capacity are
  * dropped and ARKV_STATUS_BF16_FULL or ARKV_STATUS_FP8_FULL is set.  The bits are set in
  * *dst->status. */
 #define ARKV_SEQ_FREE  (-1)

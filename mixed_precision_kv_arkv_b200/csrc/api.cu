@@ -321,8 +321,8 @@ int arkv_cache_fork(const arkv_cfg* dst_cfg, arkv_layer_cache* dst, const arkv_c
     ARKV_TRY(check_cache(src));
     if (!src_seq || !aligned(src_seq, 4)) return fail(ARKV_EINVAL, "%s: src_seq is null or misaligned", "arkv_cache_fork");
     if (dst_cfg->hkv != src_cfg->hkv || dst_cfg->head_dim != src_cfg->head_dim ||
-        dst_cfg->quant_format != src_cfg->quant_format)
-        return fail(ARKV_EINVAL, "%s: hkv, head_dim and quant_format of the two caches differ", "arkv_cache_fork");
+        dst_cfg->quant_format != src_cfg->quant_format || dst_cfg->n_obs != src_cfg->n_obs)
+        return fail(ARKV_EINVAL, "%s: hkv, head_dim, quant_format and n_obs of the two caches differ", "arkv_cache_fork");
     // (rows, and blocks of a row at least one, in 31 bits)
     if ((int64_t)dst_cfg->batch * dst_cfg->hkv > INT_MAX || (int64_t)src_cfg->batch * src_cfg->hkv > INT_MAX - (1 << 20))
         return fail(ARKV_EINVAL, "%s: batch * hkv must fit in 31 bits", "arkv_cache_fork");
