@@ -181,12 +181,19 @@ class SharedPrefix:
 
 
 def new_shared_prefix(branches: abi.arkv_cfg, cache: LayerCache, branch_start=None) -> SharedPrefix:
-    """The prefixes in `cache` for the branches described by `branches`."""
+    """The prefixes in `cache` for the branches described by `branches`.  branch_start: a list or a tensor
+    (a tensor on the device is taken as it is, its order is the caller's to keep)."""
     dev = cache.k16.device
-    if branch_start is not None:
-        branch_start = torch.as_tensor(branch_start, dtype=torch.int32, device=dev).contiguous()
-        if branch_start.numel() != cache.cfg.batch + 1:
+    if branch_start is None:
+        if cache.cfg.batch != 1:
+            raise ValueError("branch_start must be given for several prefixes")
+    else:
+        starts = torch.as_tensor(branch_start)
+        if starts.numel() != cache.cfg.batch + 1:
             raise ValueError("branch_start must have one entry per prefix and one more")
+        if starts.device.type == "cpu" and (starts.diff() < 0).any():
+            raise ValueError("branch_start must not decrease")
+        branch_start = starts.to(dtype=torch.int32, device=dev).contiguous()
     nbytes = abi.arkv_prefix_workspace_bytes(branches, cache.cfg)
     if nbytes == 0:
         raise ValueError("the branches and the prefixes do not fit together: "

@@ -101,3 +101,19 @@ def test_branch_step_refuses_prefixes_of_others():
     for prefix in (short, C.new_shared_prefix(other, mk(1, 2 * HQ, "cpu")), elsewhere):
         with pytest.raises(ValueError, match="^prefix must be"):
             branch(prefix=prefix)
+
+
+@pytest.mark.parametrize("prefixes,starts", [(2, None), (2, [0, 2]), (1, [0, 1, 3]), (2, [0, 2, 1]), (3, [0, 2, 1, 3]),
+                                             (2, torch.tensor([2, 0, 3]))])
+def test_new_shared_prefix_refuses(prefixes, starts):
+    c = C.make_cfg(B, HQ, HKV, D, 4, 4, 1.0, 0.5, 20, 30)
+    cache = C.LayerCache(C.make_cfg(prefixes, HQ, HKV, D, 4, 4, 1.0, 0.5, 9, 9), "cpu")
+    with pytest.raises(ValueError, match="^branch_start must"):
+        C.new_shared_prefix(c, cache, starts)
+
+
+@pytest.mark.parametrize("starts", [[0, 1, 3], (1, 1, 1), torch.tensor([0, 0, 3], dtype=torch.int64), [-4, 2, 90]])
+def test_new_shared_prefix_takes(starts):
+    c = C.make_cfg(B, HQ, HKV, D, 4, 4, 1.0, 0.5, 20, 30)
+    sp = C.new_shared_prefix(c, C.LayerCache(C.make_cfg(2, HQ, HKV, D, 4, 4, 1.0, 0.5, 9, 9), "cpu"), starts)
+    assert sp.branch_start.dtype == I32 and sp.branch_start.tolist() == [int(x) for x in starts]
