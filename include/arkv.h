@@ -335,7 +335,8 @@ int arkv_cache_fork(const arkv_cfg *dst_cfg, arkv_layer_cache *dst, const arkv_c
  *          the arkv_score_update that follows sees the whole softmax
  * A head without any token gets o = 0 and (M, L) = (-inf, 0).  A probability enters the
  * product with V as the sum of two bf16 parts (16 bits, as in arkv_decode_attn); sums are
- * float32.
+ * float32.  Weights are taken relative to a reference that may lie 2^32 below the largest, so
+ * for n tokens values |v^| of 2^95 / n and more can overflow before the division by L.
  * The prefix is only read: its tokens are neither scored nor reassigned while it is
  * shared (the branches' own tokens: arkv_branch_reassign).  q, o_own and o 16-byte aligned, ml 8-byte aligned; o overlaps no input.
  * Where a call sets ARKV_STATUS_TIMEOUT (in *prefix->status), its o and ml are unspecified.

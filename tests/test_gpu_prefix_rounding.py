@@ -235,3 +235,27 @@ def test_tokens_without_weight_first(cuda, d, branches, prefixes):
     o, ml = run(c, prefix, q, starts)
     check(few, (o[:-1], ml[:few.batch * hkv]), ref, 11)
     assert (o[-1] == 0).all() and (ml[few.batch * hkv:, :, 0] == float("-inf")).all() and (ml[few.batch * hkv:, :, 1] == 0).all()
+
+
+@pytest.mark.parametrize("d,fmt,branches", [(128, "e4m3", 4), (64, "e5m2", 40)])
+@pytest.mark.parametrize("up", [76, -76])
+def test_range_of_the_values(cuda, d, fmt, branches, up):
+    """Values around 2^76 and 2^-76 (n = 5000 tokens: 2^95 / n > 2^82) under logits just below the rise that moves the
+    reference, 2^30 above where it starts and as far below."""
+    n16, n8, hkv, G = 3000, 2000, 2, 4
+    pc = R.cfg(1, hkv * G, hkv, d, n16, n8, fmt=fmt)
+    prefix, u = heavy_prefix(pc, [n16], [n8], cuda, 100, heavy=0)
+    g = gen(cuda, 101)
+    fmax = 448.0 if fmt == "e4m3" else 57344.0
+    level = 30 * math.log(2.0) * (1 if up > 0 else -1)
+    for r in range(hkv):
+        k = level / math.sqrt(d) * u[r] + 0.01 * torch.randn((n16 + n8, d), generator=g, device=cuda)
+        prefix.k16[r] = k[:n16].bfloat16()
+        s = k[n16:].abs().amax(-1) / fmax
+        prefix.k8[r], prefix.sk[r] = (k[n16:] / s[:, None]).to(R.FP8[pc.quant_format]).view(torch.uint8), s
+    prefix.v16.mul_(2.0 ** up)
+    prefix.sv.mul_(2.0 ** up)
+    c = R.cfg(branches, hkv * G, hkv, d)
+    q = queries(c, u, cuda, 102, noise=0.01)
+    ref = exact(c, prefix, q, [0, branches])
+    check(c, run(c, prefix, q), ref, 79)
