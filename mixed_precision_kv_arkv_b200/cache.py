@@ -132,32 +132,28 @@ def qk_norm_rope(cfg: abi.arkv_cfg, qkv, n_tok: int, freq, k, v, q=None, q_obs=N
     """arkv_qk_norm_rope on torch tensors: qkv [batch * n_tok, >= (hq + 2 hkv) D] bf16 (unit stride in
     its last dimension), freq [rot / 2] float64 or None, k, v (and q) [batch, heads, n, D] bf16, q_obs [batch, hq,
     n_obs, D]; q_weight, k_weight [D] bf16, pos0, length [batch] int32.  All but qkv are contiguous."""
-    width = (cfg.hq + 2 * cfg.hkv) * cfg.head_dim
-    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.shape[0] != cfg.batch * n_tok or qkv.shape[1] < width:
-        raise ValueError(f"qkv must be [batch * n_tok, {width} or more] with unit stride in its last dimension")
-    if k.dim() != 4:
-        raise ValueError("k must be a contiguous [batch, heads, n, head_dim] tensor")
-    for name, t, heads in (("q", q, cfg.hq), ("k", k, cfg.hkv), ("v", v, cfg.hkv), ("q_obs", q_obs, cfg.hq)):
-        if t is None and name in ("q", "q_obs"):
-            continue
-        n = cfg.n_obs if name == "q_obs" else k.shape[2]
-        if not t.is_contiguous() or tuple(t.shape) != (cfg.batch, heads, n, cfg.head_dim):
-            raise ValueError(f"{name} must be a contiguous [batch, heads, n, head_dim] tensor")
-    for name, t in (("qkv", qkv), ("q", q), ("k", k), ("v", v), ("q_obs", q_obs)):
-        if t is not None and (t.dtype != torch.bfloat16 or t.device != qkv.device):
-            raise ValueError(f"{name} must be {torch.bfloat16} on {qkv.device}")
-    for name, t, dt, n in (("q_weight", q_weight, torch.bfloat16, cfg.head_dim),
-                           ("k_weight", k_weight, torch.bfloat16, cfg.head_dim),
-                           ("pos0", pos0, torch.int32, cfg.batch), ("length", length, torch.int32, cfg.batch)):
+    b, hq, hkv, d = cfg.batch, cfg.hq, cfg.hkv, cfg.head_dim
+    dev, bf16, width = qkv.device, torch.bfloat16, (hq + 2 * hkv) * d
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.shape[0] != b * n_tok or qkv.shape[1] < width or qkv.dtype != bf16:
+        raise ValueError(f"qkv must be {bf16} [batch * n_tok, {width} or more] with unit stride in its last dimension")
+    n = k.shape[2] if k.dim() == 4 else 0
+    for name, t, shape in (("k", k, (b, hkv, n, d)), ("v", v, (b, hkv, n, d)), ("q", q, (b, hq, n, d)),
+                           ("q_obs", q_obs, (b, hq, cfg.n_obs, d))):
+        if t is not None and (t.shape != shape or t.dtype != bf16 or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {bf16} of shape {shape} on {dev}")
+    for name, t, dt, count in (("q_weight", q_weight, bf16, d), ("k_weight", k_weight, bf16, d),
+                               ("pos0", pos0, torch.int32, b), ("length", length, torch.int32, b)):
         if t is not None:
-            _expect(name, t, dt, qkv.device, n)
+            _expect(name, t, dt, dev, count)
+    rot = 0
     if freq is not None:   # (rot <= head_dim is the library's check)
-        _expect("freq", freq, torch.float64, qkv.device, freq.numel())
+        rot = 2 * freq.numel()
+        _expect("freq", freq, torch.float64, dev, rot // 2)
     guard, s = _on_device(qkv, stream)
     with guard:
-        abi.arkv_qk_norm_rope(cfg, n_tok, qkv.data_ptr(), qkv.stride(0) if qkv.shape[0] > 1 else width, _ptr(pos0), step, _ptr(length),
-                              _ptr(q_weight), _ptr(k_weight), eps, _ptr(freq), 0 if freq is None else 2 * freq.numel(),
-                              int(bool(interleaved)), k.shape[2], _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_obs), s)
+        abi.arkv_qk_norm_rope(cfg, n_tok, qkv.data_ptr(), qkv.stride(0) if qkv.shape[0] > 1 else width, _ptr(pos0), step,
+                              _ptr(length), _ptr(q_weight), _ptr(k_weight), eps, _ptr(freq), rot, int(bool(interleaved)), n,
+                              _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_obs), s)
 
 
 def fork(dst: LayerCache, src: LayerCache, src_seq, stream=None):
