@@ -109,7 +109,7 @@ typedef struct arkv_layer_cache {
 
 /* Workspace kinds for arkv_workspace_bytes. */
 #define ARKV_WS_DECODE    0   /* arkv_decode_attn + arkv_score_update (shared, persists between them) */
-#define ARKV_WS_REASSIGN  1   /* arkv_reassign */
+#define ARKV_WS_REASSIGN  1   /* arkv_reassign, arkv_branch_reassign */
 #define ARKV_WS_PREFILL   2   /* arkv_prefill_stats and arkv_quantize_pack */
 
 /* Bytes of workspace a call needs.  n_ctx_max: the padded prefill length (the

@@ -147,7 +147,7 @@ cudaError_t launch_cache_fork(const ForkParams& p, cudaStream_t s) {
     pc.k8 = up((long long)cap_q * p.D, kPiece);
     pc.s16 = up(cap_o, kSlotsPer);
     pc.s8 = up(cap_q, kSlotsPer);
-    // A block a piece, but no more than about eight waves: rows that nobody copies (most of
+    // A block a piece, but no more than about eight waves of a B200's 148 SMs: rows that nobody copies (most of
     // them, when a few sequences of a large batch move) cost their blocks all the same (8 of 32
     // sequences replaced: 49.6 us with a block a piece, 26.6 us so).
     const long long rows = (long long)p.src_batch * p.hkv, most = (8ll * 4 * 148 + rows - 1) / rows;

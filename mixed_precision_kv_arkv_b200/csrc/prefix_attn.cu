@@ -35,11 +35,11 @@
 //
 // Bound.  HBM for one tile of rows, the tensor cores for two (floors of a prefix of
 // 23701 bf16 and 18900 FP8 tokens, 8 key heads of 128: 21.2 us for 128 rows, 26.8 us for 256).
-// Measured with the join: 48.2 and 70.8 us; 21.5 us for 5921 + 4739 tokens and 128 rows
-// (floor 5.3).  What takes the time is the issue of the softmax and the conversion: a job of
-// 128 x 64 logits takes a warp 1.0 us (bf16) to 1.4 us (FP8) with two softmax and two
-// conversion warps on each scheduler, of which a fifth is instruction fetch.  About 12 us of
-// every call are start (4 us until the first S), end of the segment, and the join.
+// Measured with the join: 59.6 and 92.1 us; 23.5 us for 5921 + 4739 tokens and 128 rows
+// (floor 5.3).  What takes the time is the issue of the softmax and the conversion, two warps of
+// each on every scheduler: 64 tokens take an SM 1.3 us with one tile of rows and 2.1 us with two,
+// and no pipe is busy for more than 37% of that.  About 11 us of every call are start, end of the
+// segment, and the join.
 //
 // Every wait is bounded: one that runs out raises ARKV_STATUS_TIMEOUT and a flag that
 // ends every role, copies and products in flight are given a last bounded wait, tensor
@@ -191,9 +191,8 @@ struct Tile {
     int fp8, idx, valid;   // kind, place in its row's segment of the cache, live tokens
 };
 
-// The tiles of a segment in order: the bf16 tiles first.  (Alternating the two kinds made the
-// softmax warps fetch their code anew all the time: 64 us against 50 for a 131072-token prefix
-// and 32 branches.)
+// The tiles of a segment in order: the bf16 tiles first.  (Alternating the two kinds makes the
+// softmax warps fetch their code anew all the time.)
 struct Tiles {
     int n, i16, e16, i8, n16, n8;
     __device__ __forceinline__ explicit Tiles(const Seg& s)   // (a whole warp)
@@ -555,7 +554,7 @@ __device__ __noinline__ void rescale(uint32_t o, float ff) {
 
 // One job: S at column s of the warp's lanes becomes P, 16 rows at a time by one piece of code
 // (32 rows at once are twice the instructions, which with the conversion's do not fit the cache
-// nearest to the schedulers: 51.6 us against 49.8 for a 42601-token prefix and 32 branches).
+// nearest to the schedulers).
 // A half is run again when its reference turns out wrong: too low, or, in a segment's first
 // job, which starts from zero, too high.  O (column o) then has to be idle: the product of the
 // job before has completed when it frees its V, entry pv.  False if that took too long.
@@ -1001,8 +1000,8 @@ __device__ void produce(const AttnArgs& a, const Ctx& cx, char* gsmem, uint32_t 
 }
 
 // Tells the join which branches have no prefix token (a CTA's share of the branches).
-// (Out of line, so that it does not lie between the loops that run all the time: 48.2 us against
-// 51.1 for a 42601-token prefix and 32 branches.)
+// (Out of line, so that it does not lie between the loops that run all the time: a 42601-token
+// prefix with 32 branches takes 63.9 us so and 65.5 inlined, but with 64 branches 97.9 and 94.8.)
 __device__ __noinline__ void no_prefix(const AttnArgs& a) {
     const LayerDims& d = a.p.d;
     for (int b = blockIdx.x * 32 + (threadIdx.x & 31); b < a.p.branches; b += gridDim.x * 32) {
@@ -1054,8 +1053,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         fence_proxy_async();
     }
     // Rows of the query tiles that no copy fills (groups of 3: 126 and 127) are zero: their logits
-    // would move references and have jobs run again (27.7 us against 22.4 for 5 prefixes of 3900
-    // tokens, 4 key heads, 23 branches).
+    // would move references and have jobs run again (27.7 us against 26.8 for 5 prefixes of 3900
+    // tokens on average, 4 key heads, 23 branches).
     for (int i = tid; i < (TWO ? 2 : 1) * (D / 64) * 128 / 16 * (kRows - a.per_tile * a.p.d.G); i += kThreads) {
         const int n = 8 * (kRows - a.per_tile * a.p.d.G);   // 16-byte pieces of 64 dimensions' rows
         *reinterpret_cast<uint4*>(smem + L::kQ + (i / n + 1) * (kRows * 128) - (i % n + 1) * 16) = make_uint4(0u, 0u, 0u, 0u);

@@ -230,7 +230,7 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s) {
     const LayerDims& d = p.d;
     const long long total = (long long)d.batch * p.n_tok;
     const int groups = kThreads / (d.D / 8);
-    // A group's start (its factors) is shared by all the heads it takes, so a block takes as many
+    // (148: a B200's SMs.)  A group's start (its factors) is shared by all the heads it takes, so a block takes as many
     // tokens as leave a group 48 heads, or two blocks an SM (8192 tokens of 48 heads: 2 tokens a
     // block 67 us, 4 54, 8 45, 16 44; 6964 of 12 heads of 64: 4 tokens 15, 16 10.8).  A call of
     // few tokens gives each a block, or several (at most a head a group), up to two an SM.
@@ -240,6 +240,8 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s) {
     // Calls of one wave (four blocks an SM) give every block the same number of tokens instead, so
     // that no SM has a block more than another, if that leaves a group 7 heads or more (48 heads of
     // 128: 4096 tokens 30.4 -> 23.1 us, 1500 tokens 15.7 -> 14.6, but 800 tokens 9.7 -> 10.1).
+    // That ends at 16 tokens a block, 9472 tokens; the waves of longer calls are uneven (9472 tokens
+    // 45.7 us, 9500 61.5, 12000 68.2, 16384 81.4, 32768 154.4 with a floor of 124.6).
     const long long wave = 4 * 148, even = (total + wave - 1) / wave;
     if (even <= kMaxTokens && even * heads >= 7 * groups) tokens = (int)even;
     const int per = groups / tokens;
@@ -255,6 +257,9 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, cudaStream_t s) {
     lc.attrs = attr;
     lc.numAttrs = 1;
     auto go = [&](auto kernel) { return cudaLaunchKernelEx(&lc, kernel, p, tokens); };
+    // kHalf shuffles whole vectors of partners; kOdd, for pairs (i, i + rot / 2) that straddle vectors, loads
+    // each partner again (8192 tokens of 48 heads of 128: 42.4 us with rot 128, 42.1 with 112, 67.0
+    // with 116, interleaved 38.1).
     const int mode = p.interleaved ? kInterleaved : (p.rot / 2) % 8 == 0 ? kHalf : kOdd;
     cudaError_t e;
     if (d.D == 128)
