@@ -259,3 +259,26 @@ def test_range_of_the_values(cuda, d, fmt, branches, up):
     q = queries(c, u, cuda, 102, noise=0.01)
     ref = exact(c, prefix, q, [0, branches])
     check(c, run(c, prefix, q), ref, 79)
+
+
+@pytest.mark.parametrize("d,G,prefixes,branches", [(128, 4, 32, 1), (64, 1, 20, 6), (64, 4, 20, 50)])
+def test_nan_and_infinite_queries_in_long_runs(cuda, d, G, prefixes, branches):
+    """Rows of NaN and infinite queries while the reference of their neighbours moves: they are NaN where the softmax
+    is, and the others' bits stay."""
+    hkv = 8
+    prefix, u = rising_prefix(R.cfg(prefixes, hkv * G, hkv, d, 515, 509, fmt="e4m3"), cuda, 110)
+    c = R.cfg(prefixes * branches, hkv * G, hkv, d)
+    starts = [branches * i for i in range(prefixes + 1)]
+    q = queries(c, u, cuda, 111, noise=0.1)
+    clean, clean_ml = run(c, prefix, q, starts)
+    hit = torch.zeros((c.batch, c.hq), dtype=torch.bool, device=cuda)
+    for i in range(0, c.batch, 5):
+        q[i, i % c.hq, 3] = float("nan")
+        q[i, (i + 3) % c.hq] = float("inf") if i % 2 else float("-inf")
+        hit[i, [i % c.hq, (i + 3) % c.hq]] = True
+    o, ml = run(c, prefix, q, starts)
+    assert torch.isnan(o[hit]).all()
+    assert torch.equal(o[~hit], clean[~hit])
+    rest = ~hit.view(c.batch * hkv, G)
+    assert torch.equal(ml[:, :G][rest], clean_ml[:, :G][rest])
+    assert int(prefix.status) == 0
